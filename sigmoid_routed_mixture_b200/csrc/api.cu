@@ -88,6 +88,8 @@ bool make_tok_maps(srm::TokMaps *m, const void *ptr, uint64_t inner, uint64_t ro
 
 }  // namespace
 
+moe_status_t srm::check_block_cfg(const moe_cfg_t *cfg) { return check_cfg(cfg, true); }
+
 extern "C" {
 
 size_t moe_workspace_size(const moe_cfg_t *cfg) {

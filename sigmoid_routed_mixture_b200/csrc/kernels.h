@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/srm_q8.h"
+
 namespace srm {
 
 constexpr int kUp = 0;    // W1|W3 contraction + SwiGLU epilogue
@@ -129,5 +131,23 @@ cudaError_t launch_dsa_scores(const CUtensorMap &tq, const CUtensorMap &tk, cons
                               int num_sms, cudaStream_t stream);
 cudaError_t launch_dsa_topk(const float *scores, int64_t B, int T, int S, int topk, int32_t *sel,
                             cudaStream_t stream);
+
+// the block's (or the dense MLP's, E == K == 0) shape rules (api.cu)
+moe_status_t check_block_cfg(const moe_cfg_t *cfg);
+
+// ---- rows in 8 bits (q8_norm.cu); strides in elements
+struct Q8RowArgs {
+  const void *x, *delta, *gamma;  // delta, gamma (no norm), x_sum and y may be null
+  void *x_sum, *y;
+  int8_t *q;
+  float *scale;
+  int64_t T, ld_x, ld_delta, ld_sum, ld_y, ld_q;
+  int H;
+  float eps;
+  int unit_offset;  // -1: row t to row t; 0 / 16: the gate / up rows of the 32-row packing units
+};
+cudaError_t launch_q8_rows(int dtype, const Q8RowArgs &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_q8_dequantize(int dtype, const int8_t *q, const float *scale, void *y, int64_t T, int H,
+                                 int64_t ld_q, int64_t ld_y, int num_sms, cudaStream_t stream);
 
 }  // namespace srm
