@@ -150,4 +150,21 @@ cudaError_t launch_q8_rows(int dtype, const Q8RowArgs &p, int num_sms, cudaStrea
 cudaError_t launch_q8_dequantize(int dtype, const int8_t *q, const float *scale, void *y, int64_t T, int H,
                                  int64_t ld_q, int64_t ld_y, int num_sms, cudaStream_t stream);
 
+// ---- rows to the experts' order and back (rows.cu); strides in elements
+struct RowsArgs {
+  int T, H, E, K, has_shared;
+  int P;  // positions: T*K + T*has_shared
+  int64_t ld_token, ld_slot, ld_residual, ld_dys;
+  int *err;
+};
+cudaError_t launch_rows_sort(const RowsArgs &p, int elem, const void *x, const float *x_scale,
+                             const int32_t *offsets, const int32_t *sorted, int32_t *pos, void *xs,
+                             float *xs_scale, int num_sms, cudaStream_t stream);
+cudaError_t launch_rows_unsort(const RowsArgs &p, int dtype, int slot_dtype, const void *ys,
+                               const float *gate, const int32_t *pos, const void *residual, void *y,
+                               int num_sms, cudaStream_t stream);
+cudaError_t launch_rows_unsort_grad(const RowsArgs &p, int dtype, int slot_dtype, const void *dy,
+                                    const void *ys, const float *gate, const int32_t *pos, void *dys,
+                                    float *dgate, int num_sms, cudaStream_t stream);
+
 }  // namespace srm
