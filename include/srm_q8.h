@@ -86,6 +86,44 @@ moe_status_t moe_q8_pack_weights(const moe_cfg_t *cfg, const void *w1, const voi
                                  const void *ws1, const void *ws3, const void *ws2, int8_t *w13_q,
                                  float *w13_scale, int8_t *w2_q, float *w2_scale, void *stream);
 
+/* Shape of a product: R rows of K elements times `groups` weight matrices of N
+ * channels.  0 <= R < 2^31 (R == 0 is a no-op), 1 <= N, groups * N < 2^31,
+ * 16 <= K <= 65536 and K % 16 == 0, 1 <= groups <= 257.
+ *   swiglu: 0, or 1: the channels are units of 16 gate and the 16 matching up
+ *           channels (moe_q8_pack_weights' w13; N % 32 == 0) and the result is
+ *           silu(gate) * up, N / 2 columns
+ *   dtype:  of y and residual: BF16, FP16 (beyond +-65504 saturated and flagged
+ *           MOE_ERR_RANGE on the device), FP32
+ *   ld_x, ld_y, ld_residual: row strides in elements; ld_x % 16 == 0. */
+typedef struct {
+    int64_t R;
+    int32_t N, K, groups, swiglu, dtype;
+    int64_t ld_x, ld_y, ld_residual;
+} moe_q8_matmul_t;
+
+/* Bytes of device workspace for this shape; 0 for an invalid one.  The first
+ * 256 bytes hold control words: zero them once when it is allocated. */
+size_t moe_q8_matmul_workspace_size(const moe_q8_matmul_t *cfg);
+
+/* Matrix product of 8-bit integers with a scale per row and per channel:
+ *     y[r][n] = x_scale[r] * w_scale[g][n] * sum_k x[r][k] w[g][n][k]
+ *               (+ residual[r][n])
+ * for the rows r in [offsets[g], offsets[g + 1]) of each group g.
+ *   x: int8 [R][K], 16-byte aligned;  x_scale: fp32 [R]
+ *   w: int8 [groups * N][K], 16-byte aligned;  w_scale: fp32 [groups * N]
+ *   offsets: int32 [groups + 1] (moe_permute's), or NULL with one group: all
+ *            rows.  Rows past offsets[groups] are left as they were.  A range
+ *            that is none is skipped and flagged MOE_ERR_BAD_INDEX.
+ *   residual: dtype [R][N] or NULL (not with swiglu); may be y itself
+ *   y: dtype [R][N], with swiglu [R][N / 2]
+ * The sum is exact; scales, silu and residual are fp32, rounded once.  A row
+ * whose scale is NaN comes out NaN.  Deterministic.  With
+ * SRM_MOE_INJECT_STALL=1 (failure-detection tests) it reports MOE_ERR_TIMEOUT
+ * like moe_expert_up. */
+moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const float *x_scale,
+                           const int8_t *w, const float *w_scale, const int32_t *offsets,
+                           const void *residual, void *y, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

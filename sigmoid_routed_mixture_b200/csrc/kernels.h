@@ -167,4 +167,33 @@ cudaError_t launch_rows_unsort_grad(const RowsArgs &p, int dtype, int slot_dtype
                                     const void *ys, const float *gate, const int32_t *pos, void *dys,
                                     float *dgate, int num_sms, cudaStream_t stream);
 
+// ---- products of 8-bit integers (q8_gemm.cu)
+constexpr int kQ8MaxGroups = 257;
+constexpr int kQ8PairRows = 256, kQ8SoloRows = 64;  // token rows per tile
+struct Q8GemmArgs {
+  const float *x_scale;    // [R]
+  const float *w_scale;    // [groups * N]
+  const int32_t *offsets;  // [groups + 1], or null: one group of all R rows
+  const void *residual;    // or null
+  void *y;
+  int64_t ld_residual, ld_y;
+  int *err;
+  int *tile_counter;       // zero before the launch, as are the split counters
+  int *split_counter;      // [tiles][CTAs of a unit][4 warps]
+  int32_t *partial;        // [units][CTAs of a unit][token column][128]
+  int R, N, K, groups;
+  int splits;              // units per tile
+  int max_mtiles;          // token blocks the workspace is laid out for
+  int y_vec, residual_vec; // rows of 16-byte multiples at 16-byte addresses
+  int stall;               // failure-detection tests only: the producer issues no loads
+};
+struct Q8Plan {
+  bool pair;
+  int splits;
+  int64_t max_mtiles, counters, partials;  // counters and partial sums in int32
+};
+Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms);
+cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const TokMaps &tok, const CUtensorMap &tw,
+                           const Q8GemmArgs &p, int num_sms, cudaStream_t stream);
+
 }  // namespace srm

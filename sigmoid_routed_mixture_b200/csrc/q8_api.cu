@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "../../include/srm_q8.h"
 #include "host_util.h"
@@ -66,9 +67,97 @@ moe_status_t run_rows(const moe_q8_rows_t *cfg, const void *x, const void *delta
   return cuda_status(srm::launch_q8_rows(cfg->dtype, a, num_sms(), s));
 }
 
+moe_status_t check_matmul(const moe_q8_matmul_t *c) {
+  if (!c) return MOE_ERR_ARG;
+  if (c->R < 0 || c->N < 1 || c->K < 1 || c->groups < 1 || !float_dtype(c->dtype)) return MOE_ERR_ARG;
+  if (c->swiglu != 0 && c->swiglu != 1) return MOE_ERR_ARG;
+  if (c->K % 16 != 0 || c->K > 65536 || (c->swiglu && c->N % 32 != 0)) return MOE_ERR_UNSUPPORTED;
+  if (c->groups > srm::kQ8MaxGroups || c->R >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(c->groups) * c->N >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  // tile numbers are 32-bit
+  const srm::Q8Plan p = srm::q8_plan(c->R, c->N, c->K, c->groups, num_sms());
+  if (p.max_mtiles * ((c->N + 127) / 128) * p.splits >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Workspace: [0, 256) control words (+0 the device error word); from 256 on the
+// tile counter and the split counters, then the partial sums.
+struct MatmulLayout {
+  size_t counters, counter_bytes, partial, total;
+};
+MatmulLayout matmul_layout(const srm::Q8Plan &p) {
+  MatmulLayout L;
+  L.counters = 256;
+  L.counter_bytes = sizeof(int) * (1 + static_cast<size_t>(p.counters));
+  L.partial = (L.counters + L.counter_bytes + 255) / 256 * 256;
+  L.total = L.partial + sizeof(int32_t) * static_cast<size_t>(p.partials);
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t moe_q8_matmul_workspace_size(const moe_q8_matmul_t *cfg) {
+  if (check_matmul(cfg) != MOE_OK) return 0;
+  return matmul_layout(srm::q8_plan(cfg->R, cfg->N, cfg->K, cfg->groups, num_sms())).total;
+}
+
+moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const float *x_scale,
+                           const int8_t *w, const float *w_scale, const int32_t *offsets,
+                           const void *residual, void *y, void *ws, size_t ws_bytes, void *stream) {
+  moe_status_t st = check_matmul(cfg);
+  if (st != MOE_OK || cfg->R == 0) return st;
+  if (!x || !x_scale || !w || !w_scale || !y || !ws || (cfg->groups > 1 && !offsets)) return MOE_ERR_ARG;
+  if (residual && cfg->swiglu) return MOE_ERR_ARG;
+  const int64_t cols = cfg->swiglu ? cfg->N / 2 : cfg->N;
+  if (!good_ld(cfg->ld_x, cfg->K) || !good_ld(cfg->ld_y, cols) ||
+      (residual && !good_ld(cfg->ld_residual, cols)))
+    return MOE_ERR_ARG;
+  const size_t e = dtype_size(cfg->dtype);
+  if (!aligned(x, 16) || cfg->ld_x % 16 != 0 || !aligned(w, 16) || !aligned(x_scale, 4) ||
+      !aligned(w_scale, 4) || (offsets && !aligned(offsets, 4)) || (residual && !aligned(residual, e)) ||
+      !aligned(y, e) || !aligned(ws, 256))
+    return MOE_ERR_ALIGN;
+  const srm::Q8Plan plan = srm::q8_plan(cfg->R, cfg->N, cfg->K, cfg->groups, num_sms());
+  const MatmulLayout L = matmul_layout(plan);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  uint8_t *wsb = static_cast<uint8_t *>(ws);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  srm::TokMaps tok;
+  CUtensorMap tw;
+  const uint64_t K = cfg->K, R = cfg->R, pitch = cfg->ld_x;
+  if (!make_tmap_8bit(&tok.small, x, K, R, pitch, static_cast<uint32_t>(srm::gemm_tok_box_rows())) ||
+      !make_tmap_8bit(&tok.big, x, K, R, pitch, static_cast<uint32_t>(srm::gemm_tok_big_box_rows())) ||
+      !make_tmap_8bit(&tw, w, K, static_cast<uint64_t>(cfg->groups) * cfg->N, K,
+                      static_cast<uint32_t>(srm::gemm_w_box_rows())))
+    return MOE_ERR_CUDA;
+  srm::Q8GemmArgs p = {};
+  p.x_scale = x_scale;
+  p.w_scale = w_scale;
+  p.offsets = offsets;
+  p.residual = residual;
+  p.y = y;
+  p.ld_residual = cfg->ld_residual;
+  p.ld_y = cfg->ld_y;
+  p.err = reinterpret_cast<int *>(wsb);
+  p.tile_counter = reinterpret_cast<int *>(wsb + L.counters);
+  p.split_counter = p.tile_counter + 1;
+  p.partial = reinterpret_cast<int32_t *>(wsb + L.partial);
+  p.R = static_cast<int>(cfg->R);
+  p.N = cfg->N;
+  p.K = cfg->K;
+  p.groups = cfg->groups;
+  p.splits = plan.splits;
+  p.max_mtiles = static_cast<int>(plan.max_mtiles);
+  p.y_vec = aligned(y, 16) && cfg->ld_y * e % 16 == 0;
+  p.residual_vec = aligned(residual, 16) && cfg->ld_residual * e % 16 == 0;
+  const char *inject = getenv("SRM_MOE_INJECT_STALL");
+  p.stall = (inject && inject[0] == '1') ? 1 : 0;
+  if (cudaMemsetAsync(p.tile_counter, 0, L.counter_bytes, s) != cudaSuccess) return MOE_ERR_CUDA;
+  return cuda_status(srm::launch_q8_gemm(cfg->swiglu != 0, cfg->dtype, plan.pair, tok, tw, p, num_sms(), s));
+}
 
 moe_status_t moe_q8_add_rmsnorm(const moe_q8_rows_t *cfg, const void *x, const void *delta,
                                 const void *gamma, float eps, void *x_sum, void *y, int8_t *q,

@@ -1,0 +1,722 @@
+// q8_gemm.cu -- products of 8-bit integers with a scale per row and per
+// channel, dense or by expert groups, on the 5th-generation tensor cores:
+//     y[r][n] = x_scale[r] * w_scale[g][n] * sum_k x[r][k] w[g][n][k] (+ residual[r][n])
+// and, with the gate and up channels interleaved 16 + 16, h = silu(gate) * up.
+// The sum is exact (tcgen05.mma kind::i8, int32 accumulators in tensor memory;
+// K <= 65536, so |sum| <= 65536 * 128 * 128 = 2^30): the result depends on
+// neither the tiling nor the order of the split reductions.
+//
+// Operand roles, tiles and barriers are those of the 16-bit grouped products
+// (grouped_gemm.cu): the weights are the MMA's M side (128 rows per CTA, 256
+// per CTA pair), the token rows its N side (a tile's rows rounded up to 32),
+// both by TMA with 128-byte swizzling, K steps of 128 bytes = 128 elements,
+// a persistent warp-specialised kernel, tiles dealt out by an atomic counter,
+// token block fastest.  A k-block moves the bytes of a 16-bit one in the same
+// MMA time and covers twice the K.
+//
+// Split reduction: with few tiles a tile's K range is cut in `splits` units.
+// Each unit's epilogue warps leave their int32 partial sums in the workspace
+// and count themselves in; the last of a tile's units adds the others' sums to
+// its own accumulator and finishes.  Nothing waits, and integer sums are exact
+// in any order, so the result does not change from run to run.
+#include <cuda.h>
+
+#include "kernels.h"
+#include "rowio.cuh"
+
+namespace srm {
+
+namespace q8 {
+constexpr int BM = 128;           // weight rows per CTA (tensor-memory lanes)
+constexpr int BK = 128;           // elements (bytes) of K per step: one swizzle atom
+constexpr int TOK_BOX = 32;       // token rows per TMA box of a tail tile
+constexpr int TOK_BOX_BIG = 128;  // ... of a full tile
+constexpr int EPI_WARPS = 4;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int MAX_GROUPS = kQ8MaxGroups;
+constexpr int MAX_STAGES = 8;
+constexpr int TILE_RING = 4;
+
+template <bool kPair>
+struct Cfg {
+  static constexpr int BT = kPair ? kQ8PairRows : kQ8SoloRows;  // token rows per tile
+  static constexpr int W_BLOCK = kPair ? 2 * BM : BM;
+  static constexpr int TOK_ROWS = kPair ? BT / 2 : BT;
+  static constexpr int STAGES = kPair ? 6 : 8;
+  static constexpr int A_BYTES = BM * BK;
+  static constexpr int B_BYTES = TOK_ROWS * BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr uint32_t TMEM_COLS = 2 * BT;
+  static constexpr uint32_t EPI_ARRIVALS = (kPair ? 2 : 1) * EPI_WARPS;
+  static constexpr int RANKS = kPair ? 2 : 1;
+};
+
+struct Smem {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t tile_full[TILE_RING];
+  uint64_t tile_empty[TILE_RING];
+  int tile_ring[TILE_RING];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int mma_consumed;
+  int total_mtiles;
+  int tile_start[MAX_GROUPS + 1];
+  int grp_off[MAX_GROUPS + 1];
+  float epi[EPI_WARPS][32][33];
+};
+template <bool kPair>
+constexpr size_t smem_bytes() {
+  return 1024 + Cfg<kPair>::STAGES * Cfg<kPair>::STAGE_BYTES + sizeof(Smem);
+}
+static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory above 227 KB");
+
+// Instruction descriptor of kind::i8: int32 accumulator (2), signed operands
+// (1), both K-major.  N is a multiple of 32, legal for single CTAs and pairs.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+struct Tile {
+  int g;         // group
+  int row_base;  // first token row
+  int rows;      // valid token rows
+  int n;         // MMA N: rows rounded up to 32
+  int w0;        // first weight row within the group
+  int id;        // tile number (splits of one tile share it)
+  int split;
+  int kb0, kb1;  // k-blocks of this unit
+};
+
+// Units: tiles in (group, weight block, token block) order, token block
+// fastest (groups of more than m_chunk token blocks in chunks, each through
+// all weight blocks), each tile's splits next to one another.
+template <bool kPair>
+__device__ __forceinline__ Tile decode(const Smem &s, const Q8GemmArgs &p, int n_tiles, int m_chunk,
+                                       int kblocks, int unit) {
+  Tile c;
+  c.id = unit / p.splits;
+  c.split = unit - c.id * p.splits;
+  c.kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * c.split / p.splits);
+  c.kb1 = static_cast<int>(static_cast<int64_t>(kblocks) * (c.split + 1) / p.splits);
+  const int mt_flat = c.id / n_tiles;
+  int lo = 0, hi = p.groups - 1;  // last g with tile_start[g] <= mt_flat
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.tile_start[mid] <= mt_flat)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int mblocks = s.tile_start[lo + 1] - s.tile_start[lo];
+  const int local = c.id - s.tile_start[lo] * n_tiles;
+  const int m0 = static_cast<int>(local / (static_cast<int64_t>(m_chunk) * n_tiles)) * m_chunk;
+  const int cm = min(m_chunk, mblocks - m0);  // token blocks in this chunk
+  const int r = local - m0 * n_tiles;
+  const int nt = r / cm;
+  const int mt = m0 + (r - nt * cm);
+  constexpr int BT = Cfg<kPair>::BT;
+  c.g = lo;
+  c.row_base = s.grp_off[lo] + mt * BT;
+  c.rows = max(0, min(BT, s.grp_off[lo + 1] - c.row_base));
+  c.n = max(32, (c.rows + 31) & ~31);
+  c.w0 = nt * Cfg<kPair>::W_BLOCK;
+  return c;
+}
+
+// Results to their type: fp16 saturates at +-65504 (flagged), as the library's
+// other fp16 intermediates do; NaN stays NaN.
+template <typename T>
+__device__ __forceinline__ float fit(float v, bool &sat) {
+  return v;
+}
+template <>
+__device__ __forceinline__ float fit<Fp16>(float v, bool &sat) {
+  if (fabsf(v) > 65504.f) {
+    sat = true;
+    v = copysignf(65504.f, v);
+  }
+  return v;
+}
+
+// silu for results of 16 bits from the hardware approximations (relative error
+// near 2^-21); with the exact exponential and division for fp32 results.
+template <typename T>
+__device__ __forceinline__ float silu(float g) {
+  return silu_approx(g);
+}
+template <>
+__device__ __forceinline__ float silu<float>(float g) {
+  return g * sigmoidf_(g);
+}
+
+// n consecutive results of one row, 16-byte stores where the row allows
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T *dst, const float (&v)[N], int n, bool vec) {
+  constexpr int E = kVec<T>;
+  if (vec && n == N) {
+#pragma unroll
+    for (int j = 0; j < N / E; ++j) {
+      float f[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = v[j * E + e];
+      RowIo<T, E>::store(dst + j * E, f);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < n) dst[j] = from_float<T>(v[j]);
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void add_row(const T *src, float (&v)[N], int n, bool vec) {
+  constexpr int E = kVec<T>;
+  if (vec && n == N) {
+#pragma unroll
+    for (int j = 0; j < N / E; ++j) {
+      float f[E];
+      RowIo<T, E>::load(src + j * E, f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[j * E + e] += f[e];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < n) v[j] += to_float(src[j]);
+  }
+}
+
+template <bool kSwiglu, bool kPair, typename T>
+__device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUtensorMap &tmap_tok_big,
+                                          const CUtensorMap &tmap_w, const Q8GemmArgs &p) {
+  using C = Cfg<kPair>;
+  constexpr int BT = C::BT;
+  constexpr uint32_t TMEM_COLS = C::TMEM_COLS;
+  constexpr int STAGES = C::STAGES;
+  constexpr int A_BYTES = C::A_BYTES;
+  constexpr int B_BYTES = C::B_BYTES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  uint8_t *base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t *sA = base;
+  uint8_t *sB = base + STAGES * A_BYTES;
+  Smem &s = *reinterpret_cast<Smem *>(base + STAGES * C::STAGE_BYTES);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0;
+  const bool leader = rank == 0;
+  const int groups = p.groups;
+  const int n_tiles = (p.N + C::W_BLOCK - 1) / C::W_BLOCK;
+  const int kblocks = (p.K + BK - 1) / BK;
+  // token blocks per chunk: about 48 MB of token rows
+  const int m_chunk = max(1, (48 << 20) / (BT * p.K));
+
+  // ---- prologue: barriers, tensor memory, per-group tile starts
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.tfull[i], 1);
+      mbar_init(&s.tempty[i], C::EPI_ARRIVALS);
+    }
+    for (int i = 0; i < TILE_RING; ++i) {
+      mbar_init(&s.tile_full[i], 1);
+      mbar_init(&s.tile_empty[i], C::EPI_ARRIVALS);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort_flag = 0;
+    s.mma_consumed = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_tok);
+    tma_prefetch_desc(&tmap_tok_big);
+    tma_prefetch_desc(&tmap_w);
+  }
+  if (warp == 1) {
+    if (kPair) {
+      tmem_alloc_pair(&s.tmem_base, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&s.tmem_base, TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  if (warp == 0) {
+    // Group offsets and an exclusive scan of ceil(rows / BT).  The offsets are
+    // the caller's: a group whose range is not 0 <= o0 <= o1 <= R, or a first
+    // offset other than 0, gets no tiles and is flagged; so is a set of ranges
+    // that together hold more rows than there are (the workspace is laid out
+    // for max_mtiles token blocks).
+    auto offset = [&](int g) { return p.offsets ? p.offsets[g] : (g == 0 ? 0 : p.R); };
+    auto token_blocks = [&](int g) {
+      const int o0 = offset(g), o1 = offset(g + 1);
+      if (o0 < 0 || o1 < o0 || o1 > p.R || (g == 0 && o0 != 0)) {
+        record_error(p.err, MOE_ERR_BAD_INDEX);
+        return 0;
+      }
+      return (o1 - o0) / BT + ((o1 - o0) % BT != 0);
+    };
+    const int per = (groups + 31) / 32;
+    const int g0 = lane * per;
+    int64_t local = 0;
+    for (int g = g0; g < min(g0 + per, groups); ++g) {
+      s.grp_off[g] = offset(g);
+      local += token_blocks(g);
+    }
+    int64_t incl = local;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    int64_t run = incl - local;
+    for (int g = g0; g < min(g0 + per, groups); ++g) {
+      s.tile_start[g] = static_cast<int>(run);  // read only if the total fits
+      run += token_blocks(g);
+    }
+    if (lane == 31) {
+      s.tile_start[groups] = static_cast<int>(incl);
+      if (incl > p.max_mtiles) {
+        record_error(p.err, MOE_ERR_BAD_INDEX);
+        incl = 0;
+      }
+      s.total_mtiles = static_cast<int>(incl);
+      s.grp_off[groups] = offset(groups);
+    }
+  }
+  tc_fence_before();
+  if (kPair)
+    cluster_sync();  // the peer's barriers are initialised before any remote use
+  else
+    __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem_base = s.tmem_base;
+  const int total_units = s.total_mtiles * n_tiles * p.splits;
+  volatile int *abort_flag = &s.abort_flag;
+  int issued = 0;  // k-blocks this CTA's producer has loaded
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer and scheduler
+    // the leader keeps LOOKAHEAD unit ids published ahead of the one it loads
+    uint32_t stage = 0, phase = 0, ts = 0, tph = 0;
+    constexpr int LOOKAHEAD = 2;
+    uint32_t ps = 0, pph = 0;
+    int published = 0, consumed = 0;
+    bool last_published = false;
+    bool pub_ok = true;
+    while (true) {
+      while (leader && !last_published && published - consumed < LOOKAHEAD) {
+        if (!mbar_wait(&s.tile_empty[ps], pph ^ 1u, abort_flag, p.err)) {
+          pub_ok = false;
+          break;
+        }
+        int t = 0;
+        if (lane == 0) {
+          t = atomicAdd(p.tile_counter, 1);
+          if (t >= total_units) t = -1;
+          s.tile_ring[ps] = t;
+          mbar_arrive(&s.tile_full[ps]);
+          if (kPair) {
+            st_shared_remote(cluster_map(&s.tile_ring[ps], 1), t);
+            mbar_arrive_remote(cluster_map(&s.tile_full[ps], 1));
+          }
+        }
+        t = __shfl_sync(0xffffffffu, t, 0);
+        last_published = t < 0;
+        ++published;
+        if (++ps == TILE_RING) {
+          ps = 0;
+          pph ^= 1u;
+        }
+      }
+      if (!pub_ok) break;
+      if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
+      ++consumed;
+      const int unit = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+      if (++ts == TILE_RING) {
+        ts = 0;
+        tph ^= 1u;
+      }
+      if (unit < 0 || p.stall) break;
+      const Tile c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, unit);
+      const int w_row = c.g * p.N + c.w0 + static_cast<int>(rank) * BM;
+      const int tok_rows = kPair ? c.n / 2 : c.n;
+      const int tok_row0 = c.row_base + static_cast<int>(rank) * tok_rows;
+      const bool big = tok_rows % TOK_BOX_BIG == 0;
+      const int box_rows = big ? TOK_BOX_BIG : TOK_BOX;
+      const CUtensorMap *tmap_b = big ? &tmap_tok_big : &tmap_tok;
+      const int nb = (tok_rows + box_rows - 1) / box_rows;
+      const uint32_t tx = (kPair ? 2u : 1u) * static_cast<uint32_t>(A_BYTES + nb * box_rows * BK);
+      bool ok = true;
+      for (int kb = c.kb0; kb < c.kb1; ++kb) {
+        if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          if (leader) mbar_arrive_expect_tx(&s.full[stage], tx);
+          uint8_t *b_dst = sB + stage * B_BYTES;
+          if (kPair) {
+            const uint32_t full_leader = cluster_map(&s.full[stage], 0);
+            tma_load_2d_pair(sA + stage * A_BYTES, &tmap_w, full_leader, kb * BK, w_row);
+            for (int j = 0; j < nb; ++j)
+              tma_load_2d_pair(b_dst + j * box_rows * BK, tmap_b, full_leader, kb * BK,
+                               tok_row0 + j * box_rows);
+          } else {
+            tma_load_2d(sA + stage * A_BYTES, &tmap_w, &s.full[stage], kb * BK, w_row);
+            for (int j = 0; j < nb; ++j)
+              tma_load_2d(b_dst + j * box_rows * BK, tmap_b, &s.full[stage], kb * BK,
+                          tok_row0 + j * box_rows);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (leader) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, ts = 0, tph = 0;
+      int consumed = 0;
+      while (true) {
+        if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err)) break;
+        const int unit = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+        if (++ts == TILE_RING) {
+          ts = 0;
+          tph ^= 1u;
+        }
+        if (unit < 0) break;
+        const Tile c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, unit);
+        const uint32_t idesc = idesc_i8(C::W_BLOCK, c.n);
+        if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BT;
+        bool ok = true;
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          if (!mbar_wait(&s.full[stage], phase, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          ++consumed;
+          if (lane == 0) {
+            const uint32_t a_addr = smem_addr(sA + stage * A_BYTES);
+            const uint32_t b_addr = smem_addr(sB + stage * B_BYTES);
+#pragma unroll
+            for (int k = 0; k < BK / 32; ++k) {
+              const uint32_t accumulate = kb != c.kb0 || k != 0 ? 1u : 0u;
+              if (kPair)
+                mma_pair(d_tmem, umma_desc_sw128(a_addr + k * 32), umma_desc_sw128(b_addr + k * 32), idesc,
+                         accumulate);
+              else
+                mma(d_tmem, umma_desc_sw128(a_addr + k * 32), umma_desc_sw128(b_addr + k * 32), idesc,
+                    accumulate);
+            }
+            if (kPair)
+              umma_commit_pair(&s.empty[stage], 0x3);
+            else
+              umma_commit(&s.empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          if (kPair)
+            umma_commit_pair(&s.tfull[acc], 0x3);
+          else
+            umma_commit(&s.tfull[acc]);
+        }
+        __syncwarp();
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (lane == 0) s.mma_consumed = consumed;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // Warp q = warp % 4 reads tensor-memory lanes 32q .. 32q+31: one weight
+    // row (channel) a lane, the tile's token rows along the columns.
+    const int q = warp & 3;
+    uint32_t acc = 0, acc_phase = 0, ts = 0, tph = 0;
+    float(&buf)[32][33] = s.epi[warp - 2];
+    while (true) {
+      if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
+      const int unit = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+      const uint32_t slot = ts;
+      if (++ts == TILE_RING) {
+        ts = 0;
+        tph ^= 1u;
+      }
+      if (unit < 0) break;
+      const Tile c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, unit);
+      const int wr = c.w0 + static_cast<int>(rank) * BM + q * 32;  // this warp's first channel
+      const float ws = wr + lane < p.N ? p.w_scale[static_cast<int64_t>(c.g) * p.N + wr + lane] : 0.f;
+      constexpr int CHUNKS = BT / 32;
+      if (!mbar_wait(&s.tfull[acc], acc_phase, abort_flag, p.err)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + acc * BT + (static_cast<uint32_t>(q * 32) << 16);
+      const bool any = wr < p.N;
+      bool mine = any;
+      // this warp's 32 lanes of a unit's partial sums: [unit][rank][column][lane]
+      constexpr int64_t SLAB = static_cast<int64_t>(BT) * BM;
+      int32_t *part0 = p.partial + (static_cast<int64_t>(c.id) * p.splits * C::RANKS + rank) * SLAB + q * 32 + lane;
+      if (p.splits > 1 && any) {
+        int32_t *dst = part0 + c.split * C::RANKS * SLAB;
+        for (int m = 0; 32 * m < c.n; ++m) {
+          uint32_t cv[32];
+          tmem_ld32(taddr + 32 * m, cv);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) __stcg(dst + (32 * m + k) * BM, static_cast<int32_t>(cv[k]));
+        }
+        __threadfence();
+        __syncwarp();
+        int seen = 0;
+        if (lane == 0) seen = atomicAdd(p.split_counter + (c.id * C::RANKS + rank) * 4 + q, 1);
+        mine = __shfl_sync(0xffffffffu, seen, 0) == p.splits - 1;
+        __threadfence();
+      }
+      bool sat = false;
+      if (mine) {
+#pragma unroll
+        for (int m = 0; m < CHUNKS; ++m) {
+          if (32 * m >= c.n) break;  // uniform across the warp
+          const int row = c.row_base + 32 * m + lane;
+          const bool live = 32 * m + lane < c.rows;
+          const float xs = live ? p.x_scale[row] : 0.f;
+          uint32_t cv[32];
+          tmem_ld32(taddr + 32 * m, cv);
+          tmem_ld_wait();
+          if (p.splits > 1) {
+            for (int o = 0; o < p.splits; ++o) {
+              if (o == c.split) continue;
+              const int32_t *src = part0 + o * C::RANKS * SLAB + 32 * m * BM;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) cv[k] += static_cast<uint32_t>(__ldcg(src + k * BM));
+            }
+          }
+          // transpose the 32 channels x 32 rows through this warp's buffer
+          // (row stride 33: both passes conflict-free): lane l then owns token
+          // row 32m + l
+#pragma unroll
+          for (int k = 0; k < 32; ++k) buf[k][lane] = static_cast<float>(static_cast<int32_t>(cv[k])) * ws;
+          __syncwarp();
+          if (live) {
+            T *y = static_cast<T *>(p.y) + static_cast<int64_t>(row) * p.ld_y;
+            if (kSwiglu) {
+              float v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                v[j] = fit<T>(silu<T>(buf[lane][j] * xs) * (buf[lane][16 + j] * xs), sat);
+              store_row<T, 16>(y + wr / 2, v, 16, p.y_vec);
+            } else {
+              const int n = min(32, p.N - wr);
+              float v[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = buf[lane][j] * xs;
+              if (p.residual)
+                add_row<T, 32>(static_cast<const T *>(p.residual) + static_cast<int64_t>(row) * p.ld_residual + wr,
+                               v, n, p.residual_vec);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = fit<T>(v[j], sat);
+              store_row<T, 32>(y + wr, v, n, p.y_vec);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (sat) record_error(p.err, MOE_ERR_RANGE);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) {
+          mbar_arrive(&s.tempty[acc]);
+          mbar_arrive(&s.tile_empty[slot]);
+        } else {
+          mbar_arrive_remote(cluster_map(&s.tempty[acc], 0));
+          mbar_arrive_remote(cluster_map(&s.tile_empty[slot], 0));
+        }
+      }
+      acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+
+  // ---- teardown.  On the error path wait (bounded) for copies and MMAs still
+  // in flight before shared and tensor memory are given back; then both CTAs
+  // of the pair meet so neither leaves while the other may still touch its
+  // shared memory.
+  __syncthreads();
+  if (s.abort_flag) {
+    if (warp == 0 && lane == 0) {
+      const uint64_t t0 = global_timer_ns();
+      if (leader) {
+        for (int i = s.mma_consumed; i < issued; ++i) {
+          const uint32_t a = smem_addr(&s.full[i % STAGES]);
+          while (!mbar_try_wait(a, static_cast<uint32_t>((i / STAGES) & 1)) &&
+                 global_timer_ns() - t0 < kWaitLimitNs) {
+          }
+        }
+      } else {
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+      }
+    }
+    if (warp == 1 && lane == 0 && leader) {
+      if (kPair)
+        umma_commit_pair(&s.drain, 0x1);
+      else
+        umma_commit(&s.drain);
+      const uint32_t a = smem_addr(&s.drain);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(a, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    if (kPair)
+      tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+template <bool kSwiglu, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    q8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_tok,
+                        const __grid_constant__ CUtensorMap tmap_tok_big,
+                        const __grid_constant__ CUtensorMap tmap_w, Q8GemmArgs p) {
+  gemm_body<kSwiglu, true, T>(tmap_tok, tmap_tok_big, tmap_w, p);
+}
+
+template <bool kSwiglu, typename T>
+__global__ void __launch_bounds__(THREADS, 1)
+    q8_gemm_solo_kernel(const __grid_constant__ CUtensorMap tmap_tok,
+                        const __grid_constant__ CUtensorMap tmap_tok_big,
+                        const __grid_constant__ CUtensorMap tmap_w, Q8GemmArgs p) {
+  gemm_body<kSwiglu, false, T>(tmap_tok, tmap_tok_big, tmap_w, p);
+}
+
+// As many CTA pairs as can be resident at once (the kernel is persistent), and
+// the shared-memory limit raised; asked once per kernel and device.
+template <typename Kern>
+cudaError_t prepare_kernel(Kern kern, size_t smem, bool pair, int num_sms, int *cached) {
+  if (*cached) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  int units = num_sms;
+  if (pair) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms & ~1);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&units, kern, &cfg) != cudaSuccess || units <= 0) units = num_sms / 2;
+  }
+  *cached = units;
+  return cudaSuccess;
+}
+
+template <bool kSwiglu, typename T>
+cudaError_t launch_t(const TokMaps &tok, const CUtensorMap &tw, const Q8GemmArgs &p, bool pair, int num_sms,
+                     cudaStream_t stream) {
+  static int cached[2][64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int &units = cached[pair ? 1 : 0][dev & 63];
+  if (pair) {
+    auto kern = q8_gemm_pair_kernel<kSwiglu, T>;
+    constexpr size_t smem = smem_bytes<true>();
+    e = prepare_kernel(kern, smem, true, num_sms, &units);
+    if (e != cudaSuccess) return e;
+    kern<<<2 * units, THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
+  } else {
+    auto kern = q8_gemm_solo_kernel<kSwiglu, T>;
+    constexpr size_t smem = smem_bytes<false>();
+    e = prepare_kernel(kern, smem, false, num_sms, &units);
+    if (e != cudaSuccess) return e;
+    kern<<<units, THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
+  }
+  return cudaGetLastError();
+}
+}  // namespace q8
+
+cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const TokMaps &tok, const CUtensorMap &tw,
+                           const Q8GemmArgs &p, int num_sms, cudaStream_t stream) {
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    return swiglu ? q8::launch_t<true, T>(tok, tw, p, pair, num_sms, stream)
+                  : q8::launch_t<false, T>(tok, tw, p, pair, num_sms, stream);
+  };
+  if (dtype == MOE_DTYPE_BF16) return go(Bf16{});
+  if (dtype == MOE_DTYPE_FP16) return go(Fp16{});
+  return go(float{});
+}
+
+// The tile shape and the split of K.  Single CTAs while a group holds few
+// rows (the weights stream, and more of their bytes are in flight), CTA pairs
+// otherwise; K is cut while the units do not fill the SMs.
+Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms) {
+  Q8Plan p;
+  const int64_t touched = R < groups ? R : groups;
+  p.pair = R >= 64 * touched + 1;
+  const int bt = p.pair ? kQ8PairRows : kQ8SoloRows, wb = p.pair ? 256 : 128;
+  const int units = p.pair ? num_sms / 2 : num_sms;
+  // ceil(rows / bt) summed over groups of R rows in all
+  p.max_mtiles = groups == 1 ? (R + bt - 1) / bt : R / bt + touched;
+  const int64_t tiles = p.max_mtiles * ((N + wb - 1) / wb);
+  const int kblocks = (K + 127) / 128;
+  p.splits = 1;
+  while (p.splits < 8 && tiles * (p.splits + 1) <= 4 * units && kblocks >= 4 * (p.splits + 1)) ++p.splits;
+  p.counters = p.splits > 1 ? tiles * 8 : 0;
+  p.partials = p.splits > 1 ? tiles * p.splits * (p.pair ? 2 : 1) * bt * 128 : 0;
+  return p;
+}
+
+}  // namespace srm

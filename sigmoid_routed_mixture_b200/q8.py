@@ -1,6 +1,7 @@
 """Thin ctypes binding of the 8-bit path in libsrm_moe.so (declared in
 include/srm_q8.h): rows in 8 bits with one scale per row, with or without the
-residual's addition and the RMSNorm.
+residual's addition and the RMSNorm, and products of 8-bit integers with a scale
+per row and per channel, dense or by expert groups.
 
 Argument marshalling only: every step runs in the library's CUDA kernels;
 PyTorch supplies device memory and the current stream of the tensors' device.
@@ -9,17 +10,23 @@ No fallback: if the library is missing, every call raises.
     q, scale = q8.add_rmsnorm(x, gamma, delta=attn_out, x_out=x, y=x_ffn)
     q, scale = q8.quantize(h)
     h = q8.dequantize(q, scale, torch.float16)
+
+    cfg = q8.MatmulConfig(R, N, K, dtype=torch.bfloat16)   # groups=, swiglu= for the experts
+    ws = q8.workspace(cfg)
+    y = q8.matmul(cfg, q, scale, w, w_scale, ws, residual=x)
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import dataclasses
 
 import torch
 
 from . import moe
 
-SYMBOLS = ("moe_q8_add_rmsnorm", "moe_q8_quantize", "moe_q8_dequantize", "moe_q8_pack_weights")
+SYMBOLS = ("moe_q8_add_rmsnorm", "moe_q8_quantize", "moe_q8_dequantize", "moe_q8_pack_weights",
+           "moe_q8_matmul_workspace_size", "moe_q8_matmul")
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3}
 
@@ -28,6 +35,12 @@ class _Rows(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("ld_x", ctypes.c_int64), ("ld_delta", ctypes.c_int64), ("ld_sum", ctypes.c_int64),
                 ("ld_y", ctypes.c_int64), ("ld_q", ctypes.c_int64)]
+
+
+class _Matmul(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("swiglu", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_residual", ctypes.c_int64)]
 
 
 _bound = False
@@ -47,6 +60,10 @@ def lib():
         L.moe_q8_dequantize.argtypes = [P(_Rows), vp, vp, vp, vp]
         L.moe_q8_pack_weights.restype = ctypes.c_int
         L.moe_q8_pack_weights.argtypes = [P(moe._Cfg)] + [vp] * 11
+        L.moe_q8_matmul_workspace_size.restype = ctypes.c_size_t
+        L.moe_q8_matmul_workspace_size.argtypes = [P(_Matmul)]
+        L.moe_q8_matmul.restype = ctypes.c_int
+        L.moe_q8_matmul.argtypes = [P(_Matmul)] + [vp] * 8 + [ctypes.c_size_t, vp]
         _bound = True
     return L
 
@@ -186,3 +203,69 @@ def pack_weights(cfg: moe.Config, w1, w3, w2, ws1=None, ws3=None, ws2=None, stre
                                              moe._ptr(w13_scale), moe._ptr(w2q), moe._ptr(w2_scale),
                                              moe._stream(stream)), "moe_q8_pack_weights")
     return w13, w13_scale, w2q, w2_scale
+
+
+# ------------------------------------------------------------------ products
+
+@dataclasses.dataclass(frozen=True)
+class MatmulConfig:
+    """R rows of K elements times `groups` weight matrices of N channels; swiglu: the channels are units of
+    16 gate and 16 up ones and the result silu(gate) * up has N / 2 columns; dtype of the result."""
+    R: int
+    N: int
+    K: int
+    groups: int = 1
+    swiglu: bool = False
+    dtype: torch.dtype = torch.bfloat16
+
+    @property
+    def columns(self) -> int:
+        return self.N // 2 if self.swiglu else self.N
+
+    def c(self, x=None, y=None, residual=None) -> _Matmul:
+        return _Matmul(self.R, self.N, self.K, self.groups, int(bool(self.swiglu)), DTYPES.get(self.dtype, -1),
+                       _ld(x), _ld(y), _ld(residual))
+
+
+def workspace_bytes(cfg: MatmulConfig) -> int:
+    n = lib().moe_q8_matmul_workspace_size(ctypes.byref(cfg.c()))
+    if n == 0:
+        raise moe.MoeError(2, "moe_q8_matmul_workspace_size")
+    return int(n)
+
+
+def workspace(cfg: MatmulConfig, device=None) -> torch.Tensor:
+    """A workspace tensor (uint8), its control words zeroed."""
+    ws = torch.empty(workspace_bytes(cfg), dtype=torch.uint8, device=device or "cuda")
+    ws[:256].zero_()
+    return ws
+
+
+def matmul(cfg: MatmulConfig, x, x_scale, w, w_scale, ws, offsets=None, residual=None, out=None, stream=None):
+    """y [R, N] (with swiglu [R, N / 2]) = x_scale * w_scale * (x . w) (+ residual).  x: int8 [R, K] with rows
+    16-byte aligned; w: int8 [groups * N, K]; offsets: int32, at least groups + 1 entries (moe.permute's),
+    or None with one group.  ``out`` may be the residual itself."""
+    _rows(x, "x", (cfg.R, cfg.K), (torch.int8,))
+    dev = x.device
+    _vector(x_scale, "x_scale", cfg.R, torch.float32, dev)
+    moe._req(w, torch.int8, (cfg.groups * cfg.N, cfg.K), "w")
+    if w.device != dev:
+        raise ValueError("w is on %s, the call on %s" % (w.device, dev))
+    _vector(w_scale, "w_scale", cfg.groups * cfg.N, torch.float32, dev)
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < cfg.groups + 1:
+            raise ValueError("offsets must have at least %d entries" % (cfg.groups + 1))
+        _vector(offsets, "offsets", offsets.numel(), torch.int32, dev)
+    if residual is not None:
+        _rows(residual, "residual", (cfg.R, cfg.columns), (cfg.dtype,), dev)
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.device != dev:
+        raise TypeError("ws must be a uint8 tensor on %s" % dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((cfg.R, cfg.columns), dtype=cfg.dtype, device=dev)
+        _rows(out, "out", (cfg.R, cfg.columns), (cfg.dtype,), dev)
+        moe._check(lib().moe_q8_matmul(ctypes.byref(cfg.c(x, out, residual)), moe._ptr(x), moe._ptr(x_scale),
+                                       moe._ptr(w), moe._ptr(w_scale), moe._ptr(offsets), moe._ptr(residual),
+                                       moe._ptr(out), moe._ptr(ws), ws.numel(), moe._stream(stream)),
+                   "moe_q8_matmul")
+    return out
