@@ -17,18 +17,17 @@ No fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 
 import torch
 
 from . import moe
+from .marshal import DTYPES, FLOATS, elsewhere, mat, on, raw_stream, rows_of, vec
+from .marshal import workspace as workspace_ptr
 
 SYMBOLS = ("moe_q8_add_rmsnorm", "moe_q8_quantize", "moe_q8_dequantize", "moe_q8_pack_weights",
            "moe_q8_matmul_workspace_size", "moe_q8_matmul")
-
-DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3}
 
 
 class _Rows(ctypes.Structure):
@@ -68,113 +67,72 @@ def lib():
     return L
 
 
-# ------------------------------------------------------------------ marshalling
-
-_NO_CONTEXT = contextlib.nullcontext()
-
-
-def _on(device, stream):
-    """Makes the tensors' device (and the call's stream, so that what the call
-    allocates belongs to it) current for the call, where it is not already."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
-        return torch.cuda.stream(stream)
-    return _NO_CONTEXT if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _rows(t, name, shape, dtypes, device=None):
-    """A matrix [T, H] with contiguous rows, `shape` None or what it has to be."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
-        raise ValueError("%s must be on a CUDA device" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, the call on %s" % (name, t.device, device))
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (name, " or ".join(map(str, dtypes)), t.dtype))
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError("%s must have shape %s, got %s" % (name, shape or "[T, H]", tuple(t.shape)))
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("%s must have contiguous rows" % name)
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError("%s must have rows that do not overlap" % name)
-    return t
-
-
-def _vector(t, name, n, dtype, device):
-    moe._req(t, dtype, (n,), name)
-    if t.device != device:
-        raise ValueError("%s is on %s, the call on %s" % (name, t.device, device))
-    return t
-
-
-def _ld(t):
-    """Row stride in elements (a single row's is free, so the row length serves)."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-FLOATS = (torch.bfloat16, torch.float16, torch.float32)
-
-
-def _q_out(out, T, H, device):
-    if out is None:
-        return (torch.empty((T, H), dtype=torch.int8, device=device),
-                torch.empty((T,), dtype=torch.float32, device=device))
-    q, scale = out
-    _rows(q, "q", (T, H), (torch.int8,), device)
-    _vector(scale, "scale", T, torch.float32, device)
-    return q, scale
-
-
 # ------------------------------------------------------------------ rows in 8 bits
+
+def _q_out(out, x, shape):
+    if out is None:
+        q, scale = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format), x.new_empty(
+            (shape[0],), dtype=torch.float32)
+        return q, q.data_ptr(), shape[1], scale, scale.data_ptr()
+    q, scale = out
+    q_ptr, ld_q = mat(q, "q", shape, torch.int8, x)
+    return q, q_ptr, ld_q, scale, vec(scale, "scale", (shape[0],), torch.float32, x)
+
 
 def add_rmsnorm(x, gamma, eps=1e-5, delta=None, x_out=None, y=None, out=None, stream=None):
     """(q int8 [T, H], scale fp32 [T]) of the RMSNorm of x (+ delta).  x, delta: bf16, fp16 or fp32
     [T, H] with contiguous rows; gamma: [H] of the same type.  ``x_out`` receives x + delta and ``y``
     the normalised rows, both in x's type; each may be x or delta itself, but not the same one.
     ``out``: (q, scale) to write into."""
-    _rows(x, "x", None, FLOATS)
-    T, H, dev = x.shape[0], x.shape[1], x.device
-    _vector(gamma, "gamma", H, x.dtype, dev)
-    for t, name in ((delta, "delta"), (x_out, "x_out"), (y, "y")):
-        if t is not None:
-            _rows(t, name, (T, H), (x.dtype,), dev)
-    with _on(dev, stream):
-        q, scale = _q_out(out, T, H, dev)
-        c = _Rows(T, H, DTYPES[x.dtype], _ld(x), _ld(delta), _ld(x_out), _ld(y), _ld(q))
-        moe._check(lib().moe_q8_add_rmsnorm(ctypes.byref(c), moe._ptr(x), moe._ptr(delta), moe._ptr(gamma),
-                                            float(eps), moe._ptr(x_out), moe._ptr(y), moe._ptr(q),
-                                            moe._ptr(scale), moe._stream(stream)), "moe_q8_add_rmsnorm")
+    if elsewhere(x, stream):
+        with on(x, stream):
+            return add_rmsnorm(x, gamma, eps, delta, x_out, y, out)
+    shape, t = rows_of(x, "x", FLOATS), x.dtype
+    x_ptr, ld = mat(x, "x", shape, t, x)
+    g_ptr = vec(gamma, "gamma", shape[1:], t, x)
+    d_ptr, ld_d = mat(delta, "delta", shape, t, x) if delta is not None else (None, 0)
+    s_ptr, ld_s = mat(x_out, "x_out", shape, t, x) if x_out is not None else (None, 0)
+    y_ptr, ld_y = mat(y, "y", shape, t, x) if y is not None else (None, 0)
+    q, q_ptr, ld_q, scale, scale_ptr = _q_out(out, x, shape)
+    c = _Rows(shape[0], shape[1], DTYPES[t], ld, ld_d, ld_s, ld_y, ld_q)
+    rc = lib().moe_q8_add_rmsnorm(c, x_ptr, d_ptr, g_ptr, eps, s_ptr, y_ptr, q_ptr, scale_ptr, raw_stream(x))
+    if rc:
+        raise moe.MoeError(rc, "moe_q8_add_rmsnorm")
     return q, scale
 
 
 def quantize(x, out=None, stream=None):
     """(q int8 [T, H], scale fp32 [T]): rows of x (bf16, fp16 or fp32) in 8 bits."""
-    _rows(x, "x", None, FLOATS)
-    T, H, dev = x.shape[0], x.shape[1], x.device
-    with _on(dev, stream):
-        q, scale = _q_out(out, T, H, dev)
-        c = _Rows(T, H, DTYPES[x.dtype], _ld(x), 0, 0, 0, _ld(q))
-        moe._check(lib().moe_q8_quantize(ctypes.byref(c), moe._ptr(x), moe._ptr(q), moe._ptr(scale),
-                                         moe._stream(stream)), "moe_q8_quantize")
+    if elsewhere(x, stream):
+        with on(x, stream):
+            return quantize(x, out)
+    shape, t = rows_of(x, "x", FLOATS), x.dtype
+    x_ptr, ld = mat(x, "x", shape, t, x)
+    q, q_ptr, ld_q, scale, scale_ptr = _q_out(out, x, shape)
+    rc = lib().moe_q8_quantize(_Rows(shape[0], shape[1], DTYPES[t], ld, 0, 0, 0, ld_q), x_ptr, q_ptr, scale_ptr,
+                               raw_stream(x))
+    if rc:
+        raise moe.MoeError(rc, "moe_q8_quantize")
     return q, scale
 
 
 def dequantize(q, scale, dtype=torch.bfloat16, out=None, stream=None):
     """The values q * scale as ``dtype`` (bf16, fp16 or fp32) [T, H]."""
-    _rows(q, "q", None, (torch.int8,))
-    T, H, dev = q.shape[0], q.shape[1], q.device
-    _vector(scale, "scale", T, torch.float32, dev)
+    if elsewhere(q, stream):
+        with on(q, stream):
+            return dequantize(q, scale, dtype, out)
+    shape = rows_of(q, "q", (torch.int8,))
     if dtype not in FLOATS:
         raise TypeError("dtype must be %s, got %s" % (" or ".join(map(str, FLOATS)), dtype))
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((T, H), dtype=dtype, device=dev)
-        _rows(out, "out", (T, H), (dtype,), dev)
-        c = _Rows(T, H, DTYPES[dtype], 0, 0, 0, _ld(out), _ld(q))
-        moe._check(lib().moe_q8_dequantize(ctypes.byref(c), moe._ptr(q), moe._ptr(scale), moe._ptr(out),
-                                           moe._stream(stream)), "moe_q8_dequantize")
+    q_ptr, ld_q = mat(q, "q", shape, torch.int8, q)
+    scale_ptr = vec(scale, "scale", shape[:1], torch.float32, q)
+    if out is None:
+        out = q.new_empty(shape, dtype=dtype)
+    y_ptr, ld_y = mat(out, "out", shape, dtype, q)
+    rc = lib().moe_q8_dequantize(_Rows(shape[0], shape[1], DTYPES[dtype], 0, 0, 0, ld_y, ld_q), q_ptr, scale_ptr,
+                                 y_ptr, raw_stream(q))
+    if rc:
+        raise moe.MoeError(rc, "moe_q8_dequantize")
     return out
 
 
@@ -191,9 +149,9 @@ def pack_weights(cfg: moe.Config, w1, w3, w2, ws1=None, ws3=None, ws2=None, stre
         moe._req(ws1, bf, (I, H), "ws1")
         moe._req(ws3, bf, (I, H), "ws3")
         moe._req(ws2, bf, (H, I), "ws2")
-    dev = (w1 if E > 0 else ws1).device
-    G = E + int(bool(cfg.has_shared))
-    with _on(dev, stream):
+    like = w1 if E > 0 else ws1
+    G, dev = E + int(bool(cfg.has_shared)), like.device
+    with on(like, stream):
         w13 = torch.empty((G * 2 * I, H), dtype=torch.int8, device=dev)
         w13_scale = torch.empty((G * 2 * I,), dtype=torch.float32, device=dev)
         w2q = torch.empty((G * H, I), dtype=torch.int8, device=dev)
@@ -201,7 +159,7 @@ def pack_weights(cfg: moe.Config, w1, w3, w2, ws1=None, ws3=None, ws2=None, stre
         moe._check(lib().moe_q8_pack_weights(ctypes.byref(cfg.c()), moe._ptr(w1), moe._ptr(w3), moe._ptr(w2),
                                              moe._ptr(ws1), moe._ptr(ws3), moe._ptr(ws2), moe._ptr(w13),
                                              moe._ptr(w13_scale), moe._ptr(w2q), moe._ptr(w2_scale),
-                                             moe._stream(stream)), "moe_q8_pack_weights")
+                                             raw_stream(like)), "moe_q8_pack_weights")
     return w13, w13_scale, w2q, w2_scale
 
 
@@ -222,9 +180,9 @@ class MatmulConfig:
     def columns(self) -> int:
         return self.N // 2 if self.swiglu else self.N
 
-    def c(self, x=None, y=None, residual=None) -> _Matmul:
+    def c(self) -> _Matmul:
         return _Matmul(self.R, self.N, self.K, self.groups, int(bool(self.swiglu)), DTYPES.get(self.dtype, -1),
-                       _ld(x), _ld(y), _ld(residual))
+                       self.K, self.columns, self.columns)
 
 
 def workspace_bytes(cfg: MatmulConfig) -> int:
@@ -245,27 +203,27 @@ def matmul(cfg: MatmulConfig, x, x_scale, w, w_scale, ws, offsets=None, residual
     """y [R, N] (with swiglu [R, N / 2]) = x_scale * w_scale * (x . w) (+ residual).  x: int8 [R, K] with rows
     16-byte aligned; w: int8 [groups * N, K]; offsets: int32, at least groups + 1 entries (moe.permute's),
     or None with one group.  ``out`` may be the residual itself."""
-    _rows(x, "x", (cfg.R, cfg.K), (torch.int8,))
-    dev = x.device
-    _vector(x_scale, "x_scale", cfg.R, torch.float32, dev)
-    moe._req(w, torch.int8, (cfg.groups * cfg.N, cfg.K), "w")
-    if w.device != dev:
-        raise ValueError("w is on %s, the call on %s" % (w.device, dev))
-    _vector(w_scale, "w_scale", cfg.groups * cfg.N, torch.float32, dev)
+    if elsewhere(x, stream):
+        with on(x, stream):
+            return matmul(cfg, x, x_scale, w, w_scale, ws, offsets, residual, out)
+    R, N, K, G, t = cfg.R, cfg.N, cfg.K, cfg.groups, cfg.dtype
+    shape = (R, N // 2 if cfg.swiglu else N)
+    x_ptr, ld_x = mat(x, "x", (R, K), torch.int8, x)
+    xs_ptr = vec(x_scale, "x_scale", (R,), torch.float32, x)
+    w_ptr = vec(w, "w", (G * N, K), torch.int8, x)
+    ws_ptr = vec(w_scale, "w_scale", (G * N,), torch.float32, x)
+    off_ptr = None
     if offsets is not None:
-        if offsets.dim() != 1 or offsets.numel() < cfg.groups + 1:
-            raise ValueError("offsets must have at least %d entries" % (cfg.groups + 1))
-        _vector(offsets, "offsets", offsets.numel(), torch.int32, dev)
-    if residual is not None:
-        _rows(residual, "residual", (cfg.R, cfg.columns), (cfg.dtype,), dev)
-    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.device != dev:
-        raise TypeError("ws must be a uint8 tensor on %s" % dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((cfg.R, cfg.columns), dtype=cfg.dtype, device=dev)
-        _rows(out, "out", (cfg.R, cfg.columns), (cfg.dtype,), dev)
-        moe._check(lib().moe_q8_matmul(ctypes.byref(cfg.c(x, out, residual)), moe._ptr(x), moe._ptr(x_scale),
-                                       moe._ptr(w), moe._ptr(w_scale), moe._ptr(offsets), moe._ptr(residual),
-                                       moe._ptr(out), moe._ptr(ws), ws.numel(), moe._stream(stream)),
-                   "moe_q8_matmul")
+        if offsets.dim() != 1 or offsets.shape[0] < G + 1:
+            raise ValueError("offsets must have at least %d entries" % (G + 1))
+        off_ptr = vec(offsets, "offsets", offsets.shape, torch.int32, x)
+    r_ptr, ld_r = mat(residual, "residual", shape, t, x) if residual is not None else (None, 0)
+    work = workspace_ptr(ws, 256, x)
+    if out is None:
+        out = x.new_empty(shape, dtype=t)
+    y_ptr, ld_y = mat(out, "out", shape, t, x)
+    c = _Matmul(R, N, K, G, 1 if cfg.swiglu else 0, DTYPES.get(t, -1), ld_x, ld_y, ld_r)
+    rc = lib().moe_q8_matmul(c, x_ptr, xs_ptr, w_ptr, ws_ptr, off_ptr, r_ptr, y_ptr, work, ws.numel(), raw_stream(x))
+    if rc:
+        raise moe.MoeError(rc, "moe_q8_matmul")
     return out

@@ -25,7 +25,8 @@ import dataclasses
 import torch
 
 from . import moe
-from .q8 import DTYPES, FLOATS, _ld, _on, _rows, _vector
+from .marshal import DTYPES, elsewhere, mat, on, raw_stream, vec
+from .marshal import workspace as workspace_ptr
 
 SYMBOLS = ("moe_rows_sort", "moe_rows_unsort", "moe_rows_sort_grad", "moe_rows_unsort_grad")
 
@@ -59,9 +60,9 @@ class Config:
         """Expert-sorted positions: T*K routed plus T shared."""
         return self.T * self.K + (self.T if self.has_shared else 0)
 
-    def c(self, token, slot, residual=None, dys=None) -> _Cfg:
-        return _Cfg(self.T, self.H, self.E, self.K, int(bool(self.has_shared)), DTYPES.get(self.dtype, -1),
-                    DTYPES.get(self.slot_dtype, -1), _ld(token), _ld(slot), _ld(residual), _ld(dys))
+    def c(self, ld_token, ld_slot, ld_residual=0, ld_dys=0) -> _Cfg:
+        return _Cfg(self.T, self.H, self.E, self.K, 1 if self.has_shared else 0, DTYPES.get(self.dtype, -1),
+                    DTYPES.get(self.slot_dtype, -1), ld_token, ld_slot, ld_residual, ld_dys)
 
 
 _bound = False
@@ -87,96 +88,95 @@ def workspace(device=None) -> torch.Tensor:
     return torch.zeros(256, dtype=torch.uint8, device=device or "cuda")
 
 
-def _ws(ws, device):
-    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.numel() < 256:
-        raise TypeError("ws must be a uint8 tensor of at least 256 bytes")
-    if ws.device != device:
-        raise ValueError("ws is on %s, the call on %s" % (ws.device, device))
-    return moe._ptr(ws)
-
-
-def _out(out, name, shape, dtype, device):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _rows(out, name, shape, (dtype,), device)
+def _pos_gate(cfg, pos, gate, like):
+    pos_ptr = vec(pos, "pos", (cfg.rows,), torch.int32, like)
+    return pos_ptr, vec(gate, "gate", (cfg.T, cfg.K), torch.float32, like) if gate is not None else None
 
 
 def sort(cfg: Config, x, offsets, sorted_, ws, x_scale=None, out=None, pos=None, xs_scale=None, stream=None):
     """Token rows x [T, H] in expert-sorted order: (xs [rows, H], pos int32 [rows]), or with the scales of
     8-bit rows (x_scale fp32 [T]) (xs, xs_scale fp32 [rows], pos).  pos is the inverse of sorted_."""
-    _rows(x, "x", (cfg.T, cfg.H), (cfg.dtype,))
-    dev = x.device
-    _vector(offsets, "offsets", cfg.E + 2, torch.int32, dev)
-    _vector(sorted_, "sorted", cfg.rows, torch.int32, dev)
+    if elsewhere(x, stream):
+        with on(x, stream):
+            return sort(cfg, x, offsets, sorted_, ws, x_scale, out, pos, xs_scale)
+    P, H, t = cfg.rows, cfg.H, cfg.dtype
+    x_ptr, ld = mat(x, "x", (cfg.T, H), t, x)
+    off_ptr = vec(offsets, "offsets", (cfg.E + 2,), torch.int32, x)
+    ids_ptr = vec(sorted_, "sorted", (P,), torch.int32, x)
+    ws_ptr = workspace_ptr(ws, 256, x)
+    xs = x.new_empty((P, H)) if out is None else out
+    xs_ptr, ld_s = mat(xs, "out", (P, H), t, x)
+    if pos is None:
+        pos = x.new_empty((P,), dtype=torch.int32)
+    pos_ptr = vec(pos, "pos", (P,), torch.int32, x)
+    scale_ptr = xs_scale_ptr = None
     if x_scale is not None:
-        _vector(x_scale, "x_scale", cfg.T, torch.float32, dev)
-    with _on(dev, stream):
-        xs = _out(out, "out", (cfg.rows, cfg.H), cfg.dtype, dev)
-        if pos is None:
-            pos = torch.empty((cfg.rows,), dtype=torch.int32, device=dev)
-        _vector(pos, "pos", cfg.rows, torch.int32, dev)
-        if x_scale is not None:
-            if xs_scale is None:
-                xs_scale = torch.empty((cfg.rows,), dtype=torch.float32, device=dev)
-            _vector(xs_scale, "xs_scale", cfg.rows, torch.float32, dev)
-        elif xs_scale is not None:
-            raise ValueError("xs_scale without x_scale")
-        moe._check(lib().moe_rows_sort(ctypes.byref(cfg.c(x, xs)), moe._ptr(x), moe._ptr(x_scale),
-                                       moe._ptr(offsets), moe._ptr(sorted_), moe._ptr(pos), moe._ptr(xs),
-                                       moe._ptr(xs_scale), _ws(ws, dev), moe._stream(stream)), "moe_rows_sort")
+        scale_ptr = vec(x_scale, "x_scale", (cfg.T,), torch.float32, x)
+        if xs_scale is None:
+            xs_scale = x.new_empty((P,), dtype=torch.float32)
+        xs_scale_ptr = vec(xs_scale, "xs_scale", (P,), torch.float32, x)
+    elif xs_scale is not None:
+        raise ValueError("xs_scale without x_scale")
+    rc = lib().moe_rows_sort(cfg.c(ld, ld_s), x_ptr, scale_ptr, off_ptr, ids_ptr, pos_ptr, xs_ptr, xs_scale_ptr,
+                             ws_ptr, raw_stream(x))
+    if rc:
+        raise moe.MoeError(rc, "moe_rows_sort")
     return (xs, pos) if x_scale is None else (xs, xs_scale, pos)
 
 
 def unsort(cfg: Config, ys, gate, pos, ws, residual=None, out=None, stream=None):
     """y [T, H] = (residual +) sum over slots of gate * ys[pos] + the shared row; gate fp32 [T, K], or None
     for weights 1.  ``out`` may be the residual itself."""
-    _rows(ys, "ys", (cfg.rows, cfg.H), (cfg.slot_dtype,))
-    dev = ys.device
-    _pos_gate(cfg, pos, gate, dev)
-    if residual is not None:
-        _rows(residual, "residual", (cfg.T, cfg.H), (cfg.dtype,), dev)
-    with _on(dev, stream):
-        y = _out(out, "out", (cfg.T, cfg.H), cfg.dtype, dev)
-        moe._check(lib().moe_rows_unsort(ctypes.byref(cfg.c(y, ys, residual)), moe._ptr(ys), moe._ptr(gate),
-                                         moe._ptr(pos), moe._ptr(residual), moe._ptr(y), _ws(ws, dev),
-                                         moe._stream(stream)), "moe_rows_unsort")
+    if elsewhere(ys, stream):
+        with on(ys, stream):
+            return unsort(cfg, ys, gate, pos, ws, residual, out)
+    shape, t = (cfg.T, cfg.H), cfg.dtype
+    ys_ptr, ld_s = mat(ys, "ys", (cfg.rows, cfg.H), cfg.slot_dtype, ys)
+    pos_ptr, gate_ptr = _pos_gate(cfg, pos, gate, ys)
+    r_ptr, ld_r = mat(residual, "residual", shape, t, ys) if residual is not None else (None, 0)
+    ws_ptr = workspace_ptr(ws, 256, ys)
+    y = ys.new_empty(shape, dtype=t) if out is None else out
+    y_ptr, ld = mat(y, "out", shape, t, ys)
+    rc = lib().moe_rows_unsort(cfg.c(ld, ld_s, ld_r), ys_ptr, gate_ptr, pos_ptr, r_ptr, y_ptr, ws_ptr, raw_stream(ys))
+    if rc:
+        raise moe.MoeError(rc, "moe_rows_unsort")
     return y
 
 
 def sort_grad(cfg: Config, dxs, pos, ws, out=None, stream=None):
     """dx [T, H] from the sorted rows' gradients dxs [rows, H] (both of cfg.dtype)."""
-    _rows(dxs, "dxs", (cfg.rows, cfg.H), (cfg.dtype,))
-    dev = dxs.device
-    _pos_gate(cfg, pos, None, dev)
-    with _on(dev, stream):
-        dx = _out(out, "out", (cfg.T, cfg.H), cfg.dtype, dev)
-        moe._check(lib().moe_rows_sort_grad(ctypes.byref(cfg.c(dx, dxs)), moe._ptr(dxs), moe._ptr(pos),
-                                            moe._ptr(dx), _ws(ws, dev), moe._stream(stream)),
-                   "moe_rows_sort_grad")
+    if elsewhere(dxs, stream):
+        with on(dxs, stream):
+            return sort_grad(cfg, dxs, pos, ws, out)
+    dxs_ptr, ld_s = mat(dxs, "dxs", (cfg.rows, cfg.H), cfg.dtype, dxs)
+    pos_ptr, _ = _pos_gate(cfg, pos, None, dxs)
+    ws_ptr = workspace_ptr(ws, 256, dxs)
+    dx = dxs.new_empty((cfg.T, cfg.H)) if out is None else out
+    dx_ptr, ld = mat(dx, "out", (cfg.T, cfg.H), cfg.dtype, dxs)
+    rc = lib().moe_rows_sort_grad(cfg.c(ld, ld_s), dxs_ptr, pos_ptr, dx_ptr, ws_ptr, raw_stream(dxs))
+    if rc:
+        raise moe.MoeError(rc, "moe_rows_sort_grad")
     return dx
 
 
 def unsort_grad(cfg: Config, dy, ys, gate, pos, ws, out=None, dgate=None, stream=None):
     """(dys [rows, H] of slot_dtype, dgate fp32 [T, K]) from dy [T, H].  ``out`` may be ys itself; rows
     that no assignment holds are left as they were."""
-    _rows(dy, "dy", (cfg.T, cfg.H), (cfg.dtype,))
-    dev = dy.device
-    _rows(ys, "ys", (cfg.rows, cfg.H), (cfg.slot_dtype,), dev)
-    _pos_gate(cfg, pos, gate, dev)
-    with _on(dev, stream):
-        dys = _out(out, "out", (cfg.rows, cfg.H), cfg.slot_dtype, dev)
-        if dgate is None:
-            dgate = torch.empty((cfg.T, cfg.K), dtype=torch.float32, device=dev)
-        moe._req(dgate, torch.float32, (cfg.T, cfg.K), "dgate")
-        moe._check(lib().moe_rows_unsort_grad(ctypes.byref(cfg.c(dy, ys, dys=dys)), moe._ptr(dy), moe._ptr(ys),
-                                              moe._ptr(gate), moe._ptr(pos), moe._ptr(dys), moe._ptr(dgate),
-                                              _ws(ws, dev), moe._stream(stream)), "moe_rows_unsort_grad")
+    if elsewhere(dy, stream):
+        with on(dy, stream):
+            return unsort_grad(cfg, dy, ys, gate, pos, ws, out, dgate)
+    slots, t = (cfg.rows, cfg.H), cfg.slot_dtype
+    dy_ptr, ld = mat(dy, "dy", (cfg.T, cfg.H), cfg.dtype, dy)
+    ys_ptr, ld_s = mat(ys, "ys", slots, t, dy)
+    pos_ptr, gate_ptr = _pos_gate(cfg, pos, gate, dy)
+    ws_ptr = workspace_ptr(ws, 256, dy)
+    dys = dy.new_empty(slots, dtype=t) if out is None else out
+    dys_ptr, ld_d = mat(dys, "out", slots, t, dy)
+    if dgate is None:
+        dgate = dy.new_empty((cfg.T, cfg.K), dtype=torch.float32)
+    dgate_ptr = vec(dgate, "dgate", (cfg.T, cfg.K), torch.float32, dy)
+    rc = lib().moe_rows_unsort_grad(cfg.c(ld, ld_s, 0, ld_d), dy_ptr, ys_ptr, gate_ptr, pos_ptr, dys_ptr, dgate_ptr,
+                                    ws_ptr, raw_stream(dy))
+    if rc:
+        raise moe.MoeError(rc, "moe_rows_unsort_grad")
     return dys, dgate
-
-
-def _pos_gate(cfg, pos, gate, device):
-    _vector(pos, "pos", cfg.rows, torch.int32, device)
-    if gate is not None:
-        moe._req(gate, torch.float32, (cfg.T, cfg.K), "gate")
-        if gate.device != device:
-            raise ValueError("gate is on %s, the call on %s" % (gate.device, device))
