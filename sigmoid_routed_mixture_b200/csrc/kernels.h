@@ -184,7 +184,6 @@ struct Q8GemmArgs {
   int R, N, K, groups;
   int splits;              // units per tile
   int max_mtiles;          // token blocks the workspace is laid out for
-  int y_vec, residual_vec; // rows of 16-byte multiples at 16-byte addresses
   int stall;               // failure-detection tests only: the producer issues no loads
 };
 struct Q8Plan {

@@ -151,8 +151,6 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
   p.groups = cfg->groups;
   p.splits = plan.splits;
   p.max_mtiles = static_cast<int>(plan.max_mtiles);
-  p.y_vec = aligned(y, 16) && cfg->ld_y * e % 16 == 0;
-  p.residual_vec = aligned(residual, 16) && cfg->ld_residual * e % 16 == 0;
   const char *inject = getenv("SRM_MOE_INJECT_STALL");
   p.stall = (inject && inject[0] == '1') ? 1 : 0;
   if (cudaMemsetAsync(p.tile_counter, 0, L.counter_bytes, s) != cudaSuccess) return MOE_ERR_CUDA;

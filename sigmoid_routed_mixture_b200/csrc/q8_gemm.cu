@@ -66,7 +66,7 @@ struct Smem {
   int total_mtiles;
   int tile_start[MAX_GROUPS + 1];
   int grp_off[MAX_GROUPS + 1];
-  float epi[EPI_WARPS][32][33];
+  alignas(16) float row_scale[EPI_WARPS][kQ8PairRows];  // each epilogue warp's copy of its tile's
 };
 template <bool kPair>
 constexpr size_t smem_bytes() {
@@ -171,42 +171,6 @@ __device__ __forceinline__ float silu(float g) {
 template <>
 __device__ __forceinline__ float silu<float>(float g) {
   return g * sigmoidf_(g);
-}
-
-// n consecutive results of one row, 16-byte stores where the row allows
-template <typename T, int N>
-__device__ __forceinline__ void store_row(T *dst, const float (&v)[N], int n, bool vec) {
-  constexpr int E = kVec<T>;
-  if (vec && n == N) {
-#pragma unroll
-    for (int j = 0; j < N / E; ++j) {
-      float f[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = v[j * E + e];
-      RowIo<T, E>::store(dst + j * E, f);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (j < n) dst[j] = from_float<T>(v[j]);
-  }
-}
-template <typename T, int N>
-__device__ __forceinline__ void add_row(const T *src, float (&v)[N], int n, bool vec) {
-  constexpr int E = kVec<T>;
-  if (vec && n == N) {
-#pragma unroll
-    for (int j = 0; j < N / E; ++j) {
-      float f[E];
-      RowIo<T, E>::load(src + j * E, f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[j * E + e] += f[e];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (j < n) v[j] += to_float(src[j]);
-  }
 }
 
 template <bool kSwiglu, bool kPair, typename T>
@@ -323,41 +287,37 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer and scheduler
-    // the leader keeps LOOKAHEAD unit ids published ahead of the one it loads
+    // A unit's CTA (or pair) starts on the unit of its own number and draws
+    // the following ones from the counter, each while its last STAGES k-blocks
+    // are still to load: late enough that no unit is taken by a CTA that is
+    // busy while another is idle, early enough to hide the counter's round
+    // trip and the signal to the peer.  (Two ids drawn ahead left 28 of 148
+    // CTAs without work, and 24 with two units, at 144 units.)
     uint32_t stage = 0, phase = 0, ts = 0, tph = 0;
-    constexpr int LOOKAHEAD = 2;
-    uint32_t ps = 0, pph = 0;
-    int published = 0, consumed = 0;
-    bool last_published = false;
-    bool pub_ok = true;
-    while (true) {
-      while (leader && !last_published && published - consumed < LOOKAHEAD) {
-        if (!mbar_wait(&s.tile_empty[ps], pph ^ 1u, abort_flag, p.err)) {
-          pub_ok = false;
-          break;
-        }
-        int t = 0;
-        if (lane == 0) {
-          t = atomicAdd(p.tile_counter, 1);
-          if (t >= total_units) t = -1;
-          s.tile_ring[ps] = t;
-          mbar_arrive(&s.tile_full[ps]);
-          if (kPair) {
-            st_shared_remote(cluster_map(&s.tile_ring[ps], 1), t);
-            mbar_arrive_remote(cluster_map(&s.tile_full[ps], 1));
-          }
-        }
-        t = __shfl_sync(0xffffffffu, t, 0);
-        last_published = t < 0;
-        ++published;
-        if (++ps == TILE_RING) {
-          ps = 0;
-          pph ^= 1u;
+    uint32_t ps = 0, pph = 0;  // next ring slot to publish and its phase
+    auto publish = [&](bool draw) {
+      if (!mbar_wait(&s.tile_empty[ps], pph ^ 1u, abort_flag, p.err)) return false;
+      if (lane == 0) {
+        int t = static_cast<int>(blockIdx.x) / C::RANKS;
+        if (draw) t = atomicAdd(p.tile_counter, 1) + static_cast<int>(gridDim.x) / C::RANKS;
+        if (t >= total_units) t = -1;
+        s.tile_ring[ps] = t;
+        mbar_arrive(&s.tile_full[ps]);
+        if (kPair) {
+          st_shared_remote(cluster_map(&s.tile_ring[ps], 1), t);
+          mbar_arrive_remote(cluster_map(&s.tile_full[ps], 1));
         }
       }
-      if (!pub_ok) break;
+      __syncwarp();
+      if (++ps == TILE_RING) {
+        ps = 0;
+        pph ^= 1u;
+      }
+      return true;
+    };
+    bool ok = !leader || publish(false);
+    while (ok) {
       if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
-      ++consumed;
       const int unit = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
       if (++ts == TILE_RING) {
         ts = 0;
@@ -373,8 +333,12 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       const CUtensorMap *tmap_b = big ? &tmap_tok_big : &tmap_tok;
       const int nb = (tok_rows + box_rows - 1) / box_rows;
       const uint32_t tx = (kPair ? 2u : 1u) * static_cast<uint32_t>(A_BYTES + nb * box_rows * BK);
-      bool ok = true;
+      const int draw_at = max(c.kb0, c.kb1 - STAGES);
       for (int kb = c.kb0; kb < c.kb1; ++kb) {
+        if (leader && kb == draw_at && !publish(true)) {
+          ok = false;
+          break;
+        }
         if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag, p.err)) {
           ok = false;
           break;
@@ -402,7 +366,6 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
           phase ^= 1u;
         }
       }
-      if (!ok) break;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
@@ -473,7 +436,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
     // row (channel) a lane, the tile's token rows along the columns.
     const int q = warp & 3;
     uint32_t acc = 0, acc_phase = 0, ts = 0, tph = 0;
-    float(&buf)[32][33] = s.epi[warp - 2];
+    float *row_scale = s.row_scale[warp - 2];
     while (true) {
       if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
       const int unit = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
@@ -486,7 +449,30 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       const Tile c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, unit);
       const int wr = c.w0 + static_cast<int>(rank) * BM + q * 32;  // this warp's first channel
       const float ws = wr + lane < p.N ? p.w_scale[static_cast<int64_t>(c.g) * p.N + wr + lane] : 0.f;
-      constexpr int CHUNKS = BT / 32;
+      // the row scales do not depend on the accumulator: read while the MMAs run
+      // (0 for the padding rows, whose results are not stored)
+      for (int r = lane; r < c.n; r += 32) row_scale[r] = r < c.rows ? p.x_scale[c.row_base + r] : 0.f;
+      __syncwarp();
+      // ... and so does the residual: a chunk's 32 rows are read a chunk ahead
+      const int ch = wr + lane;
+      const bool inside = ch < p.N;
+      T res[kSwiglu ? 1 : 32];
+      auto load_residual = [&](int m) {
+        const int live = min(32, c.rows - 32 * m);
+        const T *src = static_cast<const T *>(p.residual) + (c.row_base + 32 * m) * p.ld_residual + ch;
+        if (live == 32) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k, src += p.ld_residual) res[kSwiglu ? 0 : k] = *src;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k, src += p.ld_residual) {
+            if (k >= live) break;
+            res[kSwiglu ? 0 : k] = *src;
+          }
+        }
+      };
+      const bool add = !kSwiglu && p.residual && inside;
+      if (add) load_residual(0);
       if (!mbar_wait(&s.tfull[acc], acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + acc * BT + (static_cast<uint32_t>(q * 32) << 16);
@@ -513,12 +499,13 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       }
       bool sat = false;
       if (mine) {
-#pragma unroll
-        for (int m = 0; m < CHUNKS; ++m) {
-          if (32 * m >= c.n) break;  // uniform across the warp
-          const int row = c.row_base + 32 * m + lane;
-          const bool live = 32 * m + lane < c.rows;
-          const float xs = live ? p.x_scale[row] : 0.f;
+        for (int m = 0; 32 * m < c.n; ++m) {
+          const int64_t row0 = c.row_base + 32 * m;
+          const int live = min(32, c.rows - 32 * m);  // rows of the chunk
+          // A store covers one row's 32 channels (SwiGLU: two rows' 16
+          // features), so the accumulator needs no transpose.  Full chunks take
+          // straight-line code: a test around every store cost more than the
+          // MMAs (4096 x 6144 x 2048: 90 us with, 51 without).
           uint32_t cv[32];
           tmem_ld32(taddr + 32 * m, cv);
           tmem_ld_wait();
@@ -530,34 +517,61 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
               for (int k = 0; k < 32; ++k) cv[k] += static_cast<uint32_t>(__ldcg(src + k * BM));
             }
           }
-          // transpose the 32 channels x 32 rows through this warp's buffer
-          // (row stride 33: both passes conflict-free): lane l then owns token
-          // row 32m + l
+          float v[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) buf[k][lane] = static_cast<float>(static_cast<int32_t>(cv[k])) * ws;
-          __syncwarp();
-          if (live) {
-            T *y = static_cast<T *>(p.y) + static_cast<int64_t>(row) * p.ld_y;
-            if (kSwiglu) {
-              float v[16];
+          for (int k = 0; k < 32; k += 4) {
+            const float4 xs = *reinterpret_cast<const float4 *>(&row_scale[32 * m + k]);
+            v[k] = static_cast<float>(static_cast<int32_t>(cv[k])) * ws * xs.x;
+            v[k + 1] = static_cast<float>(static_cast<int32_t>(cv[k + 1])) * ws * xs.y;
+            v[k + 2] = static_cast<float>(static_cast<int32_t>(cv[k + 2])) * ws * xs.z;
+            v[k + 3] = static_cast<float>(static_cast<int32_t>(cv[k + 3])) * ws * xs.w;
+          }
+          if (kSwiglu) {
+            // lanes 0-15 hold the gate channels of 16 features, lanes 16-31 the
+            // up channels: of two rows, the low lanes finish the first and the
+            // high lanes the second
+            const bool high = lane >= 16;
+            T *y = static_cast<T *>(p.y) + (row0 + high) * p.ld_y + wr / 2 + (lane & 15);
+            T out[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                v[j] = fit<T>(silu<T>(buf[lane][j] * xs) * (buf[lane][16 + j] * xs), sat);
-              store_row<T, 16>(y + wr / 2, v, 16, p.y_vec);
+            for (int k = 0; k < 32; k += 2) {
+              const float got = __shfl_xor_sync(0xffffffffu, high ? v[k] : v[k + 1], 16);
+              const float gate = high ? got : v[k], up = high ? v[k + 1] : got;
+              const float h = silu<T>(gate) * up;
+              out[k / 2] = from_float<T>(fit<T>(h, sat));
+            }
+            if (live == 32) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k, y += 2 * p.ld_y) *y = out[k];
             } else {
-              const int n = min(32, p.N - wr);
-              float v[32];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = buf[lane][j] * xs;
-              if (p.residual)
-                add_row<T, 32>(static_cast<const T *>(p.residual) + static_cast<int64_t>(row) * p.ld_residual + wr,
-                               v, n, p.residual_vec);
+              for (int k = 0; k < 16; ++k, y += 2 * p.ld_y)
+                if (2 * k + high < live) *y = out[k];
+            }
+          } else if (inside) {
+            if (add) {
+              if (live == 32) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = fit<T>(v[j], sat);
-              store_row<T, 32>(y + wr, v, n, p.y_vec);
+                for (int k = 0; k < 32; ++k) v[k] += to_float(res[kSwiglu ? 0 : k]);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (k < live) v[k] += to_float(res[kSwiglu ? 0 : k]);
+              }
+              if (32 * (m + 1) < c.rows) load_residual(m + 1);
+            }
+            T *y = static_cast<T *>(p.y) + row0 * p.ld_y + ch;
+            if (live == 32) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k, y += p.ld_y) *y = from_float<T>(fit<T>(v[k], sat));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k, y += p.ld_y) {
+                if (k >= live) break;
+                *y = from_float<T>(fit<T>(v[k], sat));
+              }
             }
           }
-          __syncwarp();
         }
       }
       if (sat) record_error(p.err, MOE_ERR_RANGE);
@@ -669,19 +683,21 @@ cudaError_t launch_t(const TokMaps &tok, const CUtensorMap &tw, const Q8GemmArgs
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int &units = cached[pair ? 1 : 0][dev & 63];
+  int &resident = cached[pair ? 1 : 0][dev & 63];
+  // no more CTAs (or pairs) than units of work
+  const int64_t work = static_cast<int64_t>(p.max_mtiles) * ((p.N + (pair ? 255 : 127)) / (pair ? 256 : 128)) * p.splits;
   if (pair) {
     auto kern = q8_gemm_pair_kernel<kSwiglu, T>;
     constexpr size_t smem = smem_bytes<true>();
-    e = prepare_kernel(kern, smem, true, num_sms, &units);
+    e = prepare_kernel(kern, smem, true, num_sms, &resident);
     if (e != cudaSuccess) return e;
-    kern<<<2 * units, THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
+    kern<<<2 * static_cast<unsigned>(work < resident ? work : resident), THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
   } else {
     auto kern = q8_gemm_solo_kernel<kSwiglu, T>;
     constexpr size_t smem = smem_bytes<false>();
-    e = prepare_kernel(kern, smem, false, num_sms, &units);
+    e = prepare_kernel(kern, smem, false, num_sms, &resident);
     if (e != cudaSuccess) return e;
-    kern<<<units, THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
+    kern<<<static_cast<unsigned>(work < resident ? work : resident), THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
   }
   return cudaGetLastError();
 }
