@@ -101,9 +101,16 @@ typedef struct {
     int64_t ld_x, ld_y, ld_residual;
 } moe_q8_matmul_t;
 
-/* Bytes of device workspace for this shape; 0 for an invalid one.  The first
- * 256 bytes hold control words: zero them once when it is allocated. */
+/* Bytes of device workspace for this shape; 0 for an invalid one.  A workspace
+ * of the largest shape serves all smaller ones, one call at a time. */
 size_t moe_q8_matmul_workspace_size(const moe_q8_matmul_t *cfg);
+
+/* Sets a workspace's control words, once when it is allocated (asynchronous on
+ * `stream`); from then on the library keeps them.  In one that was not
+ * initialised (but whose first 256 bytes are zero), and in one whose call
+ * reported MOE_ERR_TIMEOUT until it is initialised again, products are correct
+ * but their work is not dealt out dynamically. */
+moe_status_t moe_q8_workspace_init(void *ws, size_t ws_bytes, void *stream);
 
 /* Matrix product of 8-bit integers with a scale per row and per channel:
  *     y[r][n] = x_scale[r] * w_scale[g][n] * sum_k x[r][k] w[g][n][k]

@@ -170,6 +170,7 @@ cudaError_t launch_rows_unsort_grad(const RowsArgs &p, int dtype, int slot_dtype
 // ---- products of 8-bit integers (q8_gemm.cu)
 constexpr int kQ8MaxGroups = 257;
 constexpr int kQ8PairRows = 256, kQ8SoloRows = 64;  // token rows per tile
+constexpr int kQ8Ready = 0x5a5a5a5a;
 struct Q8GemmArgs {
   const float *x_scale;    // [R]
   const float *w_scale;    // [groups * N]
@@ -178,18 +179,20 @@ struct Q8GemmArgs {
   void *y;
   int64_t ld_residual, ld_y;
   int *err;
-  int *tile_counter;       // zero before the launch, as are the split counters
-  int *split_counter;      // [tiles][CTAs of a unit][4 warps]
-  int32_t *partial;        // [units][CTAs of a unit][token column][128]
+  int *ready;              // kQ8Ready while the counters below are zero between calls
+  unsigned *tile_counter;
+  unsigned *part_counter;  // streamed: [tiles][CTAs of a unit][4 warps]
+  int32_t *partial;        // streamed: [units][2][CTAs of a unit][token column][128]
   int R, N, K, groups;
-  int splits;              // units per tile
+  int streamed;            // the tiles' k-blocks in equal shares (few tiles), or whole tiles
+  int units;               // CTAs (or pairs) that the work is for
   int max_mtiles;          // token blocks the workspace is laid out for
   int stall;               // failure-detection tests only: the producer issues no loads
 };
 struct Q8Plan {
-  bool pair;
-  int splits;
-  int64_t max_mtiles, counters, partials;  // counters and partial sums in int32
+  bool pair, streamed;
+  int units;
+  int64_t max_mtiles, partials;  // partial sums in int32
 };
 Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms);
 cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const TokMaps &tok, const CUtensorMap &tw,

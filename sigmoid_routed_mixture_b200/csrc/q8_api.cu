@@ -77,22 +77,22 @@ moe_status_t check_matmul(const moe_q8_matmul_t *c) {
     return MOE_ERR_UNSUPPORTED;
   // tile numbers are 32-bit
   const srm::Q8Plan p = srm::q8_plan(c->R, c->N, c->K, c->groups, num_sms());
-  if (p.max_mtiles * ((c->N + 127) / 128) * p.splits >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (p.max_mtiles * ((c->N + 127) / 128) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
-// Workspace: [0, 256) control words (+0 the device error word); from 256 on the
-// tile counter and the split counters, then the partial sums.
-struct MatmulLayout {
-  size_t counters, counter_bytes, partial, total;
-};
-MatmulLayout matmul_layout(const srm::Q8Plan &p) {
-  MatmulLayout L;
-  L.counters = 256;
-  L.counter_bytes = sizeof(int) * (1 + static_cast<size_t>(p.counters));
-  L.partial = (L.counters + L.counter_bytes + 255) / 256 * 256;
-  L.total = L.partial + sizeof(int32_t) * static_cast<size_t>(p.partials);
-  return L;
+// Workspace: control words (the device error word at 0, the tile counter at
+// 64, the ready word at 128, from 256 on the part counters), then the partial
+// sums.  The control words have the same place in every workspace, so that one
+// serves products of several shapes in turn.
+constexpr size_t kReadyOffset = 128, kPartCounters = 256;
+size_t control_bytes() {
+  // streamed work has fewer than two tiles per unit: 8 counters a tile for
+  // pairs (half as many units), 4 for single CTAs
+  return kPartCounters + sizeof(unsigned) * 8 * static_cast<size_t>((num_sms() + 31) / 32 * 32);
+}
+size_t matmul_ws_bytes(const srm::Q8Plan &p) {
+  return control_bytes() + sizeof(int32_t) * static_cast<size_t>(p.partials);
 }
 
 }  // namespace
@@ -101,7 +101,19 @@ extern "C" {
 
 size_t moe_q8_matmul_workspace_size(const moe_q8_matmul_t *cfg) {
   if (check_matmul(cfg) != MOE_OK) return 0;
-  return matmul_layout(srm::q8_plan(cfg->R, cfg->N, cfg->K, cfg->groups, num_sms())).total;
+  return matmul_ws_bytes(srm::q8_plan(cfg->R, cfg->N, cfg->K, cfg->groups, num_sms()));
+}
+
+moe_status_t moe_q8_workspace_init(void *ws, size_t ws_bytes, void *stream) {
+  if (!ws) return MOE_ERR_ARG;
+  if (!aligned(ws, 256)) return MOE_ERR_ALIGN;
+  if (ws_bytes < control_bytes()) return MOE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int byte = srm::kQ8Ready & 0xff;  // kQ8Ready is four times the same byte
+  if (cudaMemsetAsync(ws, 0, control_bytes(), s) != cudaSuccess ||
+      cudaMemsetAsync(static_cast<uint8_t *>(ws) + kReadyOffset, byte, sizeof(int), s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const float *x_scale,
@@ -121,8 +133,7 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
       !aligned(y, e) || !aligned(ws, 256))
     return MOE_ERR_ALIGN;
   const srm::Q8Plan plan = srm::q8_plan(cfg->R, cfg->N, cfg->K, cfg->groups, num_sms());
-  const MatmulLayout L = matmul_layout(plan);
-  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < matmul_ws_bytes(plan)) return MOE_ERR_WORKSPACE;
   uint8_t *wsb = static_cast<uint8_t *>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   srm::TokMaps tok;
@@ -142,18 +153,19 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
   p.ld_residual = cfg->ld_residual;
   p.ld_y = cfg->ld_y;
   p.err = reinterpret_cast<int *>(wsb);
-  p.tile_counter = reinterpret_cast<int *>(wsb + L.counters);
-  p.split_counter = p.tile_counter + 1;
-  p.partial = reinterpret_cast<int32_t *>(wsb + L.partial);
+  p.ready = reinterpret_cast<int *>(wsb + kReadyOffset);
+  p.tile_counter = reinterpret_cast<unsigned *>(wsb + 64);
+  p.part_counter = reinterpret_cast<unsigned *>(wsb + kPartCounters);
+  p.partial = reinterpret_cast<int32_t *>(wsb + control_bytes());
   p.R = static_cast<int>(cfg->R);
   p.N = cfg->N;
   p.K = cfg->K;
   p.groups = cfg->groups;
-  p.splits = plan.splits;
+  p.streamed = plan.streamed;
+  p.units = plan.units;
   p.max_mtiles = static_cast<int>(plan.max_mtiles);
   const char *inject = getenv("SRM_MOE_INJECT_STALL");
   p.stall = (inject && inject[0] == '1') ? 1 : 0;
-  if (cudaMemsetAsync(p.tile_counter, 0, L.counter_bytes, s) != cudaSuccess) return MOE_ERR_CUDA;
   return cuda_status(srm::launch_q8_gemm(cfg->swiglu != 0, cfg->dtype, plan.pair, tok, tw, p, num_sms(), s));
 }
 

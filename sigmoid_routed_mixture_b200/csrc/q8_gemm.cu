@@ -14,11 +14,20 @@
 // token block fastest.  A k-block moves the bytes of a 16-bit one in the same
 // MMA time and covers twice the K.
 //
-// Split reduction: with few tiles a tile's K range is cut in `splits` units.
-// Each unit's epilogue warps leave their int32 partial sums in the workspace
-// and count themselves in; the last of a tile's units adds the others' sums to
-// its own accumulator and finishes.  Nothing waits, and integer sums are exact
-// in any order, so the result does not change from run to run.
+// Streamed reduction: with few tiles the tiles' k-blocks, laid end to end, are
+// dealt to the CTAs (or pairs) in equal contiguous shares, so that all of them
+// read weights until the end whatever the tile count.  A share starts and ends
+// inside tiles: for such a part the epilogue warps leave their int32 partial
+// sums in the workspace and count themselves in, and the last of a tile's
+// parts to arrive adds the others' sums to its own accumulator and finishes.
+// Nothing waits, and integer sums are exact in any order, so the result does
+// not change from run to run.
+//
+// The counters return to zero by themselves (each wraps at its last arrival),
+// so a call needs no clearing launch before it (1 to 3 us of a decode
+// product).  The workspace's ready word says that they can be trusted: it is
+// set when a workspace is initialised and taken back by a call that gave up a
+// wait.  Without it the tiles are dealt out whole and in a fixed stride.
 #include <cuda.h>
 
 #include "kernels.h"
@@ -62,6 +71,7 @@ struct Smem {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  int ready;
   int mma_consumed;
   int total_mtiles;
   int tile_start[MAX_GROUPS + 1];
@@ -106,22 +116,20 @@ struct Tile {
   int rows;      // valid token rows
   int n;         // MMA N: rows rounded up to 32
   int w0;        // first weight row within the group
-  int id;        // tile number (splits of one tile share it)
-  int split;
-  int kb0, kb1;  // k-blocks of this unit
+  int id;        // tile number
+  int kb0, kb1;  // k-blocks of it to do here (all of them unless streamed)
 };
 
-// Units: tiles in (group, weight block, token block) order, token block
-// fastest (groups of more than m_chunk token blocks in chunks, each through
-// all weight blocks), each tile's splits next to one another.
+// Tiles in (group, weight block, token block) order, token block fastest
+// (groups of more than m_chunk token blocks in chunks, each through all weight
+// blocks).
 template <bool kPair>
 __device__ __forceinline__ Tile decode(const Smem &s, const Q8GemmArgs &p, int n_tiles, int m_chunk,
-                                       int kblocks, int unit) {
+                                       int kblocks, int tile) {
   Tile c;
-  c.id = unit / p.splits;
-  c.split = unit - c.id * p.splits;
-  c.kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * c.split / p.splits);
-  c.kb1 = static_cast<int>(static_cast<int64_t>(kblocks) * (c.split + 1) / p.splits);
+  c.id = tile;
+  c.kb0 = 0;
+  c.kb1 = kblocks;
   const int mt_flat = c.id / n_tiles;
   int lo = 0, hi = p.groups - 1;  // last g with tile_start[g] <= mt_flat
   while (lo < hi) {
@@ -146,6 +154,37 @@ __device__ __forceinline__ Tile decode(const Smem &s, const Q8GemmArgs &p, int n
   c.w0 = nt * Cfg<kPair>::W_BLOCK;
   return c;
 }
+
+// A unit's share of the streamed k-blocks: [begin(u), begin(u + 1)) of
+// tiles * kblocks, walked part by part (a part lies in one tile).
+struct Stream {
+  int64_t total, pos, end;
+  int units, kblocks;
+  __device__ __forceinline__ Stream(int64_t tiles, int kblocks_, int units_, int unit)
+      : total(tiles * kblocks_), pos(0), end(0), units(units_), kblocks(kblocks_) {
+    if (total < units) units = static_cast<int>(total);  // no share is empty
+    if (unit < units) {
+      pos = begin(unit);
+      end = begin(unit + 1);
+    }
+  }
+  __device__ __forceinline__ int64_t begin(int unit) const { return unit * total / units; }
+  // the unit whose share holds k-block q: the last u with u * total / units <= q
+  __device__ __forceinline__ int unit_of(int64_t q) const {
+    return static_cast<int>(((q + 1) * units - 1) / total);
+  }
+  template <bool kPair>
+  __device__ __forceinline__ bool next(const Smem &s, const Q8GemmArgs &p, int n_tiles, int m_chunk, Tile *c) {
+    if (pos >= end) return false;
+    const int tile = static_cast<int>(pos / kblocks);
+    *c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, tile);
+    c->kb0 = static_cast<int>(pos - static_cast<int64_t>(tile) * kblocks);
+    const int64_t left = end - pos;
+    if (left < kblocks - c->kb0) c->kb1 = c->kb0 + static_cast<int>(left);
+    pos += c->kb1 - c->kb0;
+    return true;
+  }
+};
 
 // Results to their type: fp16 saturates at +-65504 (flagged), as the library's
 // other fp16 intermediates do; NaN stays NaN.
@@ -215,6 +254,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
     }
     mbar_init(&s.drain, 1);
     s.abort_flag = 0;
+    s.ready = *p.ready == kQ8Ready;
     s.mma_consumed = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmap_tok);
@@ -281,26 +321,34 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
   tc_fence_after();
 
   const uint32_t tmem_base = s.tmem_base;
-  const int total_units = s.total_mtiles * n_tiles * p.splits;
+  const int total_tiles = s.total_mtiles * n_tiles;
+  const bool counted = s.ready != 0;
+  const bool streamed = p.streamed && counted;
+  Stream stream(total_tiles, kblocks, static_cast<int>(gridDim.x) / C::RANKS,
+                static_cast<int>(blockIdx.x) / C::RANKS);
   volatile int *abort_flag = &s.abort_flag;
   int issued = 0;  // k-blocks this CTA's producer has loaded
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer and scheduler
-    // A unit's CTA (or pair) starts on the unit of its own number and draws
-    // the following ones from the counter, each while its last STAGES k-blocks
-    // are still to load: late enough that no unit is taken by a CTA that is
-    // busy while another is idle, early enough to hide the counter's round
-    // trip and the signal to the peer.  (Two ids drawn ahead left 28 of 148
-    // CTAs without work, and 24 with two units, at 144 units.)
+    // A CTA (or pair) starts on the tile of its own number and draws the
+    // following ones from the counter, each while its last STAGES k-blocks are
+    // still to load: late enough that no tile is taken by a CTA that is busy
+    // while another is idle, early enough to hide the counter's round trip and
+    // the signal to the peer.  (Two ids drawn ahead left 28 of 148 CTAs
+    // without work, and 24 with two tiles, at 144 tiles.)
     uint32_t stage = 0, phase = 0, ts = 0, tph = 0;
     uint32_t ps = 0, pph = 0;  // next ring slot to publish and its phase
+    int last = static_cast<int>(blockIdx.x) / C::RANKS;  // the newest tile of this unit
     auto publish = [&](bool draw) {
       if (!mbar_wait(&s.tile_empty[ps], pph ^ 1u, abort_flag, p.err)) return false;
       if (lane == 0) {
-        int t = static_cast<int>(blockIdx.x) / C::RANKS;
-        if (draw) t = atomicAdd(p.tile_counter, 1) + static_cast<int>(gridDim.x) / C::RANKS;
-        if (t >= total_units) t = -1;
+        const int stride = static_cast<int>(gridDim.x) / C::RANKS;
+        int t = last;
+        if (draw)  // as many draws as tiles: the last one leaves the counter at 0
+          t = counted ? static_cast<int>(atomicInc(p.tile_counter, total_tiles - 1)) + stride : last + stride;
+        last = t;
+        if (t >= total_tiles) t = -1;
         s.tile_ring[ps] = t;
         mbar_arrive(&s.tile_full[ps]);
         if (kPair) {
@@ -315,16 +363,21 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       }
       return true;
     };
-    bool ok = !leader || publish(false);
-    while (ok) {
-      if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
-      const int unit = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
-      if (++ts == TILE_RING) {
-        ts = 0;
-        tph ^= 1u;
+    bool ok = streamed || !leader || publish(false);
+    while (ok && !p.stall) {
+      Tile c;
+      if (streamed) {
+        if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
+      } else {
+        if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
+        const int tile = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+        if (++ts == TILE_RING) {
+          ts = 0;
+          tph ^= 1u;
+        }
+        if (tile < 0) break;
+        c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, tile);
       }
-      if (unit < 0 || p.stall) break;
-      const Tile c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, unit);
       const int w_row = c.g * p.N + c.w0 + static_cast<int>(rank) * BM;
       const int tok_rows = kPair ? c.n / 2 : c.n;
       const int tok_row0 = c.row_base + static_cast<int>(rank) * tok_rows;
@@ -335,7 +388,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       const uint32_t tx = (kPair ? 2u : 1u) * static_cast<uint32_t>(A_BYTES + nb * box_rows * BK);
       const int draw_at = max(c.kb0, c.kb1 - STAGES);
       for (int kb = c.kb0; kb < c.kb1; ++kb) {
-        if (leader && kb == draw_at && !publish(true)) {
+        if (leader && !streamed && kb == draw_at && !publish(true)) {
           ok = false;
           break;
         }
@@ -373,14 +426,19 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, ts = 0, tph = 0;
       int consumed = 0;
       while (true) {
-        if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err)) break;
-        const int unit = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
-        if (++ts == TILE_RING) {
-          ts = 0;
-          tph ^= 1u;
+        Tile c;
+        if (streamed) {
+          if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
+        } else {
+          if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err)) break;
+          const int tile = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+          if (++ts == TILE_RING) {
+            ts = 0;
+            tph ^= 1u;
+          }
+          if (tile < 0) break;
+          c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, tile);
         }
-        if (unit < 0) break;
-        const Tile c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, unit);
         const uint32_t idesc = idesc_i8(C::W_BLOCK, c.n);
         if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
         tc_fence_after();
@@ -438,15 +496,20 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
     uint32_t acc = 0, acc_phase = 0, ts = 0, tph = 0;
     float *row_scale = s.row_scale[warp - 2];
     while (true) {
-      if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
-      const int unit = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+      Tile c;
       const uint32_t slot = ts;
-      if (++ts == TILE_RING) {
-        ts = 0;
-        tph ^= 1u;
+      if (streamed) {
+        if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
+      } else {
+        if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
+        const int tile = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+        if (++ts == TILE_RING) {
+          ts = 0;
+          tph ^= 1u;
+        }
+        if (tile < 0) break;
+        c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, tile);
       }
-      if (unit < 0) break;
-      const Tile c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, unit);
       const int wr = c.w0 + static_cast<int>(rank) * BM + q * 32;  // this warp's first channel
       const float ws = wr + lane < p.N ? p.w_scale[static_cast<int64_t>(c.g) * p.N + wr + lane] : 0.f;
       // the row scales do not depend on the accumulator: read while the MMAs run
@@ -477,12 +540,21 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       tc_fence_after();
       const uint32_t taddr = tmem_base + acc * BT + (static_cast<uint32_t>(q * 32) << 16);
       const bool any = wr < p.N;
+      const bool part = c.kb1 - c.kb0 < kblocks;
       bool mine = any;
-      // this warp's 32 lanes of a unit's partial sums: [unit][rank][column][lane]
+      // a part's sums: [unit][its first or another part][CTA][column][lane]
       constexpr int64_t SLAB = static_cast<int64_t>(BT) * BM;
-      int32_t *part0 = p.partial + (static_cast<int64_t>(c.id) * p.splits * C::RANKS + rank) * SLAB + q * 32 + lane;
-      if (p.splits > 1 && any) {
-        int32_t *dst = part0 + c.split * C::RANKS * SLAB;
+      const int unit = static_cast<int>(blockIdx.x) / C::RANKS;
+      const int64_t tile0 = static_cast<int64_t>(c.id) * kblocks;
+      int first_unit = unit, last_unit = unit;
+      auto slab = [&](int u) {
+        const int later = stream.begin(u) < tile0 ? 1 : 0;  // the unit starts in an earlier tile
+        return p.partial + ((static_cast<int64_t>(u) * 2 + later) * C::RANKS + rank) * SLAB + q * 32 + lane;
+      };
+      if (part && any) {
+        first_unit = stream.unit_of(tile0);
+        last_unit = stream.unit_of(tile0 + kblocks - 1);
+        int32_t *dst = slab(unit);
         for (int m = 0; 32 * m < c.n; ++m) {
           uint32_t cv[32];
           tmem_ld32(taddr + 32 * m, cv);
@@ -493,8 +565,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
         __threadfence();
         __syncwarp();
         int seen = 0;
-        if (lane == 0) seen = atomicAdd(p.split_counter + (c.id * C::RANKS + rank) * 4 + q, 1);
-        mine = __shfl_sync(0xffffffffu, seen, 0) == p.splits - 1;
+        if (lane == 0)
+          seen = static_cast<int>(
+              atomicInc(p.part_counter + (c.id * C::RANKS + rank) * 4 + q, last_unit - first_unit));
+        mine = __shfl_sync(0xffffffffu, seen, 0) == last_unit - first_unit;
         __threadfence();
       }
       bool sat = false;
@@ -509,13 +583,11 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
           uint32_t cv[32];
           tmem_ld32(taddr + 32 * m, cv);
           tmem_ld_wait();
-          if (p.splits > 1) {
-            for (int o = 0; o < p.splits; ++o) {
-              if (o == c.split) continue;
-              const int32_t *src = part0 + o * C::RANKS * SLAB + 32 * m * BM;
+          for (int u = first_unit; u <= last_unit; ++u) {
+            if (u == unit) continue;
+            const int32_t *src = slab(u) + 32 * m * BM;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) cv[k] += static_cast<uint32_t>(__ldcg(src + k * BM));
-            }
+            for (int k = 0; k < 32; ++k) cv[k] += static_cast<uint32_t>(__ldcg(src + k * BM));
           }
           float v[32];
 #pragma unroll
@@ -580,10 +652,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       if (lane == 0) {
         if (leader) {
           mbar_arrive(&s.tempty[acc]);
-          mbar_arrive(&s.tile_empty[slot]);
+          if (!streamed) mbar_arrive(&s.tile_empty[slot]);
         } else {
           mbar_arrive_remote(cluster_map(&s.tempty[acc], 0));
-          mbar_arrive_remote(cluster_map(&s.tile_empty[slot], 0));
+          if (!streamed) mbar_arrive_remote(cluster_map(&s.tile_empty[slot], 0));
         }
       }
       acc ^= 1u;
@@ -597,6 +669,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
   // shared memory.
   __syncthreads();
   if (s.abort_flag) {
+    if (threadIdx.x == 0) atomicExch(p.ready, 0);
     if (warp == 0 && lane == 0) {
       const uint64_t t0 = global_timer_ns();
       if (leader) {
@@ -684,20 +757,18 @@ cudaError_t launch_t(const TokMaps &tok, const CUtensorMap &tw, const Q8GemmArgs
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   int &resident = cached[pair ? 1 : 0][dev & 63];
-  // no more CTAs (or pairs) than units of work
-  const int64_t work = static_cast<int64_t>(p.max_mtiles) * ((p.N + (pair ? 255 : 127)) / (pair ? 256 : 128)) * p.splits;
   if (pair) {
     auto kern = q8_gemm_pair_kernel<kSwiglu, T>;
     constexpr size_t smem = smem_bytes<true>();
     e = prepare_kernel(kern, smem, true, num_sms, &resident);
     if (e != cudaSuccess) return e;
-    kern<<<2 * static_cast<unsigned>(work < resident ? work : resident), THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
+    kern<<<2 * static_cast<unsigned>(p.units < resident ? p.units : resident), THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
   } else {
     auto kern = q8_gemm_solo_kernel<kSwiglu, T>;
     constexpr size_t smem = smem_bytes<false>();
     e = prepare_kernel(kern, smem, false, num_sms, &resident);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(work < resident ? work : resident), THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
+    kern<<<static_cast<unsigned>(p.units < resident ? p.units : resident), THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
   }
   return cudaGetLastError();
 }
@@ -715,23 +786,38 @@ cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const TokMaps &tok
   return go(float{});
 }
 
-// The tile shape and the split of K.  Single CTAs while a group holds few
-// rows (the weights stream, and more of their bytes are in flight), CTA pairs
-// otherwise; K is cut while the units do not fill the SMs.
+// The tile shape, and how the work is dealt out.
+//   CTA pairs or single CTAs: a k-block takes about the same time in either
+//   (0.27 and 0.29 us) and a pair's covers four times the products per CTA,
+//   but a single CTA's tile starts and ends sooner.  Single ones while a group
+//   holds at most 64 rows (64 x 24576 x 6144: 38 us against 42), and while all
+//   their tiles run at once (777 x 1001 x 2064: 14 against 19 us); pairs above
+//   (256 x 6144 x 12288: 40 against 53).
+//   Streamed shares while the tiles do not fill the units twice.  With no more
+//   tiles than units each tile is cut into equal parts, so many that a further
+//   one would cost more (about 2 us of exchange for single CTAs, 6 for pairs)
+//   than its share of the tile's k-blocks; otherwise the shares straddle tiles
+//   (1 x 24576 x 6144, 192 tiles: 33 us against 38 dealt out whole).
 Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms) {
   Q8Plan p;
   const int64_t touched = R < groups ? R : groups;
-  p.pair = R >= 64 * touched + 1;
+  // ceil(rows / bt) summed over groups of R rows in all, at most
+  auto blocks = [&](int bt) { return groups == 1 ? (R + bt - 1) / bt : R / bt + touched; };
+  p.pair = R > kQ8SoloRows * touched && blocks(kQ8SoloRows) * ((N + 127) / 128) > num_sms;
   const int bt = p.pair ? kQ8PairRows : kQ8SoloRows, wb = p.pair ? 256 : 128;
   const int units = p.pair ? num_sms / 2 : num_sms;
-  // ceil(rows / bt) summed over groups of R rows in all
-  p.max_mtiles = groups == 1 ? (R + bt - 1) / bt : R / bt + touched;
+  p.max_mtiles = blocks(bt);
   const int64_t tiles = p.max_mtiles * ((N + wb - 1) / wb);
-  const int kblocks = (K + 127) / 128;
-  p.splits = 1;
-  while (p.splits < 8 && tiles * (p.splits + 1) <= 4 * units && kblocks >= 4 * (p.splits + 1)) ++p.splits;
-  p.counters = p.splits > 1 ? tiles * 8 : 0;
-  p.partials = p.splits > 1 ? tiles * p.splits * (p.pair ? 2 : 1) * bt * 128 : 0;
+  const int64_t kblocks = (K + 127) / 128;
+  p.streamed = tiles < 2 * units;
+  p.units = tiles < units ? static_cast<int>(tiles) : units;
+  if (tiles > 0 && tiles <= units) {
+    const int64_t cost = p.pair ? 21 : 7;  // k-blocks' time that a further part costs
+    int64_t parts = 1;
+    while ((parts + 1) * parts * cost <= kblocks && (parts + 1) * tiles <= units) ++parts;
+    p.units = static_cast<int>(parts * tiles);
+  }
+  p.partials = p.streamed ? static_cast<int64_t>(p.units) * 2 * (p.pair ? 2 : 1) * bt * 128 : 0;
   return p;
 }
 

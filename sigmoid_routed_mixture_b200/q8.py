@@ -27,7 +27,7 @@ from .marshal import DTYPES, FLOATS, elsewhere, mat, on, raw_stream, rows_of, ve
 from .marshal import workspace as workspace_ptr
 
 SYMBOLS = ("moe_q8_add_rmsnorm", "moe_q8_quantize", "moe_q8_dequantize", "moe_q8_pack_weights",
-           "moe_q8_matmul_workspace_size", "moe_q8_matmul")
+           "moe_q8_matmul_workspace_size", "moe_q8_workspace_init", "moe_q8_matmul")
 
 
 class _Rows(ctypes.Structure):
@@ -61,6 +61,8 @@ def lib():
         L.moe_q8_pack_weights.argtypes = [P(moe._Cfg)] + [vp] * 11
         L.moe_q8_matmul_workspace_size.restype = ctypes.c_size_t
         L.moe_q8_matmul_workspace_size.argtypes = [P(_Matmul)]
+        L.moe_q8_workspace_init.restype = ctypes.c_int
+        L.moe_q8_workspace_init.argtypes = [vp, ctypes.c_size_t, vp]
         L.moe_q8_matmul.restype = ctypes.c_int
         L.moe_q8_matmul.argtypes = [P(_Matmul)] + [vp] * 8 + [ctypes.c_size_t, vp]
         _bound = True
@@ -192,11 +194,19 @@ def workspace_bytes(cfg: MatmulConfig) -> int:
     return int(n)
 
 
-def workspace(cfg: MatmulConfig, device=None) -> torch.Tensor:
-    """A workspace tensor (uint8), its control words zeroed."""
-    ws = torch.empty(workspace_bytes(cfg), dtype=torch.uint8, device=device or "cuda")
-    ws[:256].zero_()
+def workspace(*cfgs: MatmulConfig, device=None) -> torch.Tensor:
+    """An initialised workspace tensor (uint8) that serves products of these shapes, one at a time."""
+    ws = torch.empty(max(workspace_bytes(c) for c in cfgs), dtype=torch.uint8, device=device or "cuda")
+    init_workspace(ws)
     return ws
+
+
+def init_workspace(ws):
+    """Sets a workspace's control words: once for memory allocated elsewhere, and after a call that
+    reported MOE_ERR_TIMEOUT."""
+    with on(ws, None):
+        moe._check(lib().moe_q8_workspace_init(workspace_ptr(ws, 256, ws), ws.numel(), raw_stream(ws)),
+                   "moe_q8_workspace_init")
 
 
 def matmul(cfg: MatmulConfig, x, x_scale, w, w_scale, ws, offsets=None, residual=None, out=None, stream=None):

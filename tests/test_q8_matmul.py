@@ -55,6 +55,8 @@ def test_pointers_refused():
     need = q8.lib().moe_q8_matmul_workspace_size(ctypes.byref(c))
     assert call(c, n=need - 1) == 4
     assert call(c_cfg(R=0), **{k: None for k in ("x", "xs", "w", "ws_", "off", "y", "ws")}) == 0
+    init = q8.lib().moe_q8_workspace_init
+    assert init(None, 1 << 20, None) == 1 and init(ODD, 1 << 20, None) == 3 and init(A, 256, None) == 4
     assert q8.lib().moe_q8_matmul(None, A, A, A, A, A, None, A, A, 1 << 40, None) == 1
 
 
@@ -231,7 +233,7 @@ def test_streams_graphs_and_shared_workspaces():
     """Two captured products of the same workspace, replayed in turn on one stream; and an empty product."""
     g = gen(8)
     small, large = q8.MatmulConfig(8, 512, 4096), q8.MatmulConfig(300, 512, 4096)
-    work = torch.zeros(max(q8.workspace_bytes(small), q8.workspace_bytes(large)), dtype=torch.uint8, device="cuda")
+    work = q8.workspace(small, large)
     w, ws = ints(g, 512, 4096), scales(g, 512)
     xa, xb, sa, sb = ints(g, 8, 4096), ints(g, 300, 4096), scales(g, 8), scales(g, 300)
     s = torch.cuda.Stream()
@@ -267,7 +269,28 @@ def test_timeout_is_reported_and_context_survives(R, monkeypatch):
     q8.matmul(cfg, x, xs, w, ws, work)
     assert moe.device_error(work) == 6
     monkeypatch.delenv("SRM_MOE_INJECT_STALL")
+    for _ in range(2):
+        check(q8.matmul(cfg, x, xs, w, ws, work), x, xs, w, ws)
+    q8.init_workspace(work)
     check(q8.matmul(cfg, x, xs, w, ws, work), x, xs, w, ws)
+    assert moe.device_error(work) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,N,K", [(5, 700, 2048), (64, 24576, 1024), (300, 1000, 4096), (3000, 4096, 256)])
+def test_workspace_without_its_control_words(R, N, K):
+    """Only the first 256 bytes zero, the rest anything: whole tiles in a fixed stride, the same results."""
+    g = gen(11)
+    cfg = q8.MatmulConfig(R, N, K)
+    x, w, xs, ws = ints(g, R, K), ints(g, N, K), scales(g, R), scales(g, N)
+    good = q8.matmul(cfg, x, xs, w, ws, q8.workspace(cfg))
+    work = torch.randint(0, 256, (q8.workspace_bytes(cfg),), generator=g, device="cuda", dtype=torch.uint8)
+    work[:256] = 0
+    for _ in range(2):
+        assert torch.equal(q8.matmul(cfg, x, xs, w, ws, work), good)
+    q8.init_workspace(work)
+    for _ in range(3):  # the counters are back at zero after each call
+        assert torch.equal(q8.matmul(cfg, x, xs, w, ws, work), good)
     assert moe.device_error(work) == 0
 
 
