@@ -148,7 +148,7 @@ struct Q8RowArgs {
 };
 cudaError_t launch_q8_rows(int dtype, const Q8RowArgs &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_q8_dequantize(int dtype, const int8_t *q, const float *scale, void *y, int64_t T, int H,
-                                 int64_t ld_q, int64_t ld_y, int num_sms, cudaStream_t stream);
+                                 int64_t ld_q, int64_t ld_y, cudaStream_t stream);
 
 // ---- rows to the experts' order and back (rows.cu); strides in elements
 struct RowsArgs {

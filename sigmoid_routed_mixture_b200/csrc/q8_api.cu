@@ -196,7 +196,7 @@ moe_status_t moe_q8_dequantize(const moe_q8_rows_t *cfg, const int8_t *q, const 
   if (!good_ld(cfg->ld_q, cfg->H) || !good_ld(cfg->ld_y, cfg->H)) return MOE_ERR_ARG;
   if (!aligned(y, dtype_size(cfg->dtype)) || !aligned(scale, 4)) return MOE_ERR_ALIGN;
   return cuda_status(srm::launch_q8_dequantize(cfg->dtype, q, scale, y, cfg->T, cfg->H, cfg->ld_q, cfg->ld_y,
-                                               num_sms(), static_cast<cudaStream_t>(stream)));
+                                               static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_q8_pack_weights(const moe_cfg_t *cfg, const void *w1, const void *w3, const void *w2,

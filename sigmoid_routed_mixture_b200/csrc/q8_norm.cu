@@ -9,6 +9,8 @@
 // (U loads of E elements a thread) through its two reductions, the sum of
 // squares and the maximum, so the bytes are the floor's.  Rows that do not fit
 // (more than 1024 threads x U x E elements) are read three times.
+#include <type_traits>
+
 #include "kernels.h"
 #include "rowio.cuh"
 
@@ -61,22 +63,29 @@ __device__ __forceinline__ QScale q_scale(uint32_t max_bits) {
   s.r = m > 0.f ? 127.f / (m * s.up) : 0.f;
   return s;
 }
-__device__ __forceinline__ int q_of(float n, const QScale &s) {
-  return s.finite ? max(-127, min(127, __float2int_rn((n * s.up) * s.r))) : 0;
+
+// Adding 1.5 * 2^23 rounds n * r to the nearest integer (ties to even) in the
+// sum's low bits, in one operation: |n * r| <= 127 (1 + 2^-22), so the low
+// byte is q in two's complement and needs no clamp.
+__device__ __forceinline__ uint32_t q_bits(float n, float r) { return __float_as_uint(fmaf(n, r, 12582912.f)); }
+
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// E consecutive q of a row that is finite and not under 2^-100 (n scaled by up).
 template <int E>
-__device__ __forceinline__ void store_q(int8_t *p, const float (&n)[E], const QScale &s) {
-  if (E == 1) {
-    *p = static_cast<int8_t>(q_of(n[0], s));
+__device__ __forceinline__ void store_q(int8_t *p, const float (&n)[E], float r) {
+  if constexpr (E == 1) {
+    *p = static_cast<int8_t>(q_bits(n[0], r));
   } else {
-    uint32_t w[(E + 3) / 4];
+    uint32_t w[E / 4];
 #pragma unroll
     for (int k = 0; k < E / 4; ++k)
-      w[k] = (q_of(n[4 * k], s) & 0xff) | (q_of(n[4 * k + 1], s) & 0xff) << 8 |
-             (q_of(n[4 * k + 2], s) & 0xff) << 16 | q_of(n[4 * k + 3], s) << 24;
-    if (E == 8)
-      *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[E / 4 - 1]);
+      w[k] = low_bytes(q_bits(n[4 * k], r), q_bits(n[4 * k + 1], r), q_bits(n[4 * k + 2], r),
+                       q_bits(n[4 * k + 3], r));
+    if constexpr (E == 8)
+      *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     else
       *reinterpret_cast<uint32_t *>(p) = w[0];
   }
@@ -91,9 +100,12 @@ __device__ __forceinline__ int64_t dst_row(int64_t t, int unit_offset) {
 }  // namespace
 
 // kWarps == 1: a warp per row (several rows a CTA); otherwise a CTA per row.
-template <typename T, int E, int U, int kWarps>
-__global__ void __launch_bounds__(kWarps == 1 ? 128 : 1024)
+// All of a row's loads (x, delta, gamma) are in flight before the first use.
+// kPlain: quantisation alone (no delta, gamma, x_sum or y), in fewer registers.
+template <typename T, int E, int U, int kWarps, bool kPlain>
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     q8_rows_kernel(const Q8RowArgs p) {
+  using Io = RowIo<T, E>;
   __shared__ float sum_buf[2][32];
   __shared__ uint32_t max_buf[32];
   const int tid = kWarps == 1 ? (threadIdx.x & 31) : threadIdx.x;
@@ -101,34 +113,54 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 1024)
   const int64_t t = kWarps == 1 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : blockIdx.x;
   if (t >= p.T) return;  // whole warps (or CTAs) only
   const T *x = static_cast<const T *>(p.x) + t * p.ld_x;
-  const T *delta = p.delta ? static_cast<const T *>(p.delta) + t * p.ld_delta : nullptr;
-  const T *gamma = static_cast<const T *>(p.gamma);
-  float v[U][E];
+  const T *delta = !kPlain && p.delta ? static_cast<const T *>(p.delta) + t * p.ld_delta : nullptr;
+  const T *gamma = kPlain ? nullptr : static_cast<const T *>(p.gamma);
+  typename Io::Raw rx[U], rd[U], rg[U];
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int i = (j * tpr + tid) * E;
-#pragma unroll
-    for (int k = 0; k < E; ++k) v[j][k] = 0.f;
-    if (i < p.H) RowIo<T, E>::load(x + i, v[j]);
+    if (i < p.H) rx[j] = *reinterpret_cast<const typename Io::Raw *>(x + i);
   }
   if (delta) {
-    T *x_sum = p.x_sum ? static_cast<T *>(p.x_sum) + t * p.ld_sum : nullptr;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int i = (j * tpr + tid) * E;
-      if (i < p.H) {
+      if (i < p.H) rd[j] = *reinterpret_cast<const typename Io::Raw *>(delta + i);
+    }
+  }
+  if (gamma) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = (j * tpr + tid) * E;
+      if (i < p.H) rg[j] = *reinterpret_cast<const typename Io::Raw *>(gamma + i);
+    }
+  }
+  float v[U][E];
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    if ((j * tpr + tid) * E < p.H) {
+      Io::unpack(rx[j], v[j]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[j][k] = 0.f;
+    }
+  }
+  if (delta) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if ((j * tpr + tid) * E < p.H) {
         float d[E];
-        RowIo<T, E>::load(delta + i, d);
+        Io::unpack(rd[j], d);
 #pragma unroll
         for (int k = 0; k < E; ++k) v[j][k] = to_float(from_float<T>(v[j][k] + d[k]));
-        if (x_sum) RowIo<T, E>::store(x_sum + i, v[j]);
       }
     }
-  } else if (p.x_sum) {
+  }
+  if (!kPlain && p.x_sum) {
     T *x_sum = static_cast<T *>(p.x_sum) + t * p.ld_sum;
 #pragma unroll
     for (int j = 0; j < U; ++j)
-      if ((j * tpr + tid) * E < p.H) RowIo<T, E>::store(x_sum + (j * tpr + tid) * E, v[j]);
+      if ((j * tpr + tid) * E < p.H) Io::store(x_sum + (j * tpr + tid) * E, v[j]);
   }
   if (gamma) {
     float ss = 0.f;
@@ -154,10 +186,9 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 1024)
     const float inv = 1.0f / sqrtf(ms);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int i = (j * tpr + tid) * E;
-      if (i < p.H) {
+      if ((j * tpr + tid) * E < p.H) {
         float g[E];
-        RowIo<T, E>::load(gamma + i, g);
+        Io::unpack(rg[j], g);
 #pragma unroll
         for (int k = 0; k < E; ++k) v[j][k] = v[j][k] * inv * g[k];
       }
@@ -169,19 +200,26 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 1024)
 #pragma unroll
     for (int k = 0; k < E; ++k)
       if ((j * tpr + tid) * E < p.H) m = max(m, abs_bits(v[j][k]));
+  if (!kPlain && p.y) {
+    T *y = static_cast<T *>(p.y) + t * p.ld_y;
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if ((j * tpr + tid) * E < p.H) Io::store(y + (j * tpr + tid) * E, v[j]);
+  }
   const QScale s = q_scale(row_max<kWarps>(m, max_buf));
   const int64_t to = dst_row(t, p.unit_offset);
   if (tid == 0) p.scale[to] = s.scale;
   int8_t *q = p.q + to * p.ld_q;
-  T *y = p.y ? static_cast<T *>(p.y) + t * p.ld_y : nullptr;
+  if (!s.finite || s.up != 1.f) {  // rare, and the same in the whole row
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const int i = (j * tpr + tid) * E;
-    if (i < p.H) {
-      store_q<E>(q + i, v[j], s);
-      if (y) RowIo<T, E>::store(y + i, v[j]);
-    }
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[j][k] = s.finite ? v[j][k] * s.up : 0.f;
   }
+  const float r = s.finite ? s.r : 0.f;
+#pragma unroll
+  for (int j = 0; j < U; ++j)
+    if ((j * tpr + tid) * E < p.H) store_q<E>(q + (j * tpr + tid) * E, v[j], r);
 }
 
 // Rows too long for one CTA's registers: element loads, three passes over the
@@ -222,60 +260,81 @@ __global__ void __launch_bounds__(1024) q8_long_rows_kernel(const Q8RowArgs p) {
     const float v = at(i), n = normed(i, v);
     if (p.x_sum) static_cast<T *>(p.x_sum)[t * p.ld_sum + i] = from_float<T>(v);
     if (p.y) static_cast<T *>(p.y)[t * p.ld_y + i] = from_float<T>(n);
-    p.q[to * p.ld_q + i] = static_cast<int8_t>(q_of(n, s));
+    p.q[to * p.ld_q + i] = s.finite ? static_cast<int8_t>(q_bits(n * s.up, s.r)) : int8_t(0);
   }
 }
 
-// y = q * scale: E elements a thread, rows of ceil(H / E) threads.
+// y = q * scale.  tpr threads (a power of two) share a row, each with kBatch
+// loads of E elements in flight; 256 / tpr rows a CTA.
 template <typename T, int E>
 __global__ void __launch_bounds__(256)
     q8_dequantize_kernel(const int8_t *q, const float *scale, T *y, int64_t T_, int H, int64_t ld_q,
-                         int64_t ld_y) {
-  const int per_row = (H + E - 1) / E;
-  const int64_t total = T_ * per_row;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t t = i / per_row;
-    const int c = static_cast<int>(i - t * per_row) * E;
-    const float s = scale[t];
-    float f[E];
-    if (E == 1) {
-      f[0] = q[t * ld_q + c] * s;
-    } else {
-      uint32_t w[(E + 3) / 4];
-      if (E == 8) {
-        const uint2 r = *reinterpret_cast<const uint2 *>(q + t * ld_q + c);
-        w[0] = r.x;
-        w[E / 4 - 1] = r.y;
-      } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(q + t * ld_q + c);
-      }
+                         int64_t ld_y, int tpr_log2) {
+  constexpr int kBatch = 4;
+  using Word = typename std::conditional<E == 8, uint2, typename std::conditional<E == 4, uint32_t, int8_t>::type>::type;
+  const int tpr = 1 << tpr_log2;
+  const int tid = threadIdx.x & (tpr - 1);
+  const int64_t t = (static_cast<int64_t>(blockIdx.x) << (8 - tpr_log2)) + (threadIdx.x >> tpr_log2);
+  if (t >= T_) return;
+  const int8_t *src = q + t * ld_q;
+  T *dst = y + t * ld_y;
+  const float s = scale[t];
+  for (int i0 = tid * E; i0 < H; i0 += kBatch * tpr * E) {
+    Word w[kBatch];
 #pragma unroll
-      for (int k = 0; k < E; ++k)
-        f[k] = static_cast<float>(static_cast<int8_t>(w[k / 4] >> (8 * (k % 4)))) * s;
+    for (int j = 0; j < kBatch; ++j)
+      if (i0 + j * tpr * E < H) w[j] = *reinterpret_cast<const Word *>(src + i0 + j * tpr * E);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (i0 + j * tpr * E >= H) break;
+      float f[E];
+      if constexpr (E == 1) {
+        f[0] = w[j] * s;
+      } else {
+        uint32_t u[E / 4];
+        if constexpr (E == 8) {
+          u[0] = w[j].x;
+          u[1] = w[j].y;
+        } else {
+          u[0] = w[j];
+        }
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          f[k] = static_cast<float>(static_cast<int8_t>(u[k / 4] >> (8 * (k % 4)))) * s;
+      }
+      RowIo<T, E>::store(dst + i0 + j * tpr * E, f);
     }
-    RowIo<T, E>::store(y + t * ld_y + c, f);
   }
 }
 
 namespace {
 
-template <typename T, int E, int U>
+template <typename T, int E, int U, bool kPlain>
 cudaError_t launch_rows_u(const Q8RowArgs &p, cudaStream_t stream) {
   const int loads = (p.H + E - 1) / E;
-  if (loads <= 32 * U) {
-    q8_rows_kernel<T, E, U, 1><<<static_cast<unsigned>((p.T + 3) / 4), 128, 0, stream>>>(p);
-  } else {
-    const int threads = ((loads + U - 1) / U + 31) & ~31;
-    q8_rows_kernel<T, E, U, 32><<<static_cast<unsigned>(p.T), threads, 0, stream>>>(p);
-  }
+  const int threads = ((loads + U - 1) / U + 31) & ~31;
+  const unsigned rows = static_cast<unsigned>(p.T);
+  constexpr int kMost = E == 1 && U > 1 ? 16 : 32;  // warps a CTA may need
+  if (threads <= 32)
+    q8_rows_kernel<T, E, U, 1, kPlain><<<(rows + 3) / 4, 128, 0, stream>>>(p);
+  else if (threads <= 256)  // the fewer threads, the more registers each may have
+    q8_rows_kernel<T, E, U, 8, kPlain><<<rows, threads, 0, stream>>>(p);
+  else if (threads <= 512)
+    q8_rows_kernel<T, E, U, 16, kPlain><<<rows, threads, 0, stream>>>(p);
+  else
+    q8_rows_kernel<T, E, U, kMost, kPlain><<<rows, threads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int E>
 cudaError_t launch_rows_e(const Q8RowArgs &p, int num_sms, cudaStream_t stream) {
+  constexpr int U = E == 1 ? 16 : 4;  // loads a thread: 16 elements at least
   const int loads = (p.H + E - 1) / E;
-  if (loads <= 1024 && p.T <= 2 * num_sms) return launch_rows_u<T, E, 1>(p, stream);
-  if (loads <= 4 * 1024) return launch_rows_u<T, E, 4>(p, stream);
+  const bool plain = !p.delta && !p.gamma && !p.x_sum && !p.y;
+  if (loads <= 1024 && p.T <= 2 * num_sms)
+    return plain ? launch_rows_u<T, E, 1, true>(p, stream) : launch_rows_u<T, E, 1, false>(p, stream);
+  if (loads <= U * (E == 1 ? 512 : 1024))
+    return plain ? launch_rows_u<T, E, U, true>(p, stream) : launch_rows_u<T, E, U, false>(p, stream);
   q8_long_rows_kernel<T><<<static_cast<unsigned>(p.T), 1024, 0, stream>>>(p);
   return cudaGetLastError();
 }
@@ -296,17 +355,18 @@ cudaError_t launch_rows_t(const Q8RowArgs &p, int num_sms, cudaStream_t stream) 
 
 template <typename T>
 cudaError_t launch_dequant_t(const int8_t *q, const float *scale, void *y, int64_t T_, int H,
-                             int64_t ld_q, int64_t ld_y, int num_sms, cudaStream_t stream) {
+                             int64_t ld_q, int64_t ld_y, cudaStream_t stream) {
   constexpr int E = kVec<T>;
   const bool vec = H % E == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0 && ld_y % E == 0 &&
                    reinterpret_cast<uintptr_t>(q) % E == 0 && ld_q % E == 0;
-  const int64_t total = T_ * ((H + (vec ? E : 1) - 1) / (vec ? E : 1));
-  const int64_t cap = num_sms * 16ll;
-  const unsigned blocks = static_cast<unsigned>((total + 255) / 256 < cap ? (total + 255) / 256 : cap);
+  const int loads = vec ? H / E : H;
+  int log2 = 0;  // threads per row: four loads each
+  while (log2 < 8 && (4 << log2) < loads) ++log2;
+  const unsigned blocks = static_cast<unsigned>((T_ + (256 >> log2) - 1) >> (8 - log2));
   if (vec)
-    q8_dequantize_kernel<T, E><<<blocks, 256, 0, stream>>>(q, scale, static_cast<T *>(y), T_, H, ld_q, ld_y);
+    q8_dequantize_kernel<T, E><<<blocks, 256, 0, stream>>>(q, scale, static_cast<T *>(y), T_, H, ld_q, ld_y, log2);
   else
-    q8_dequantize_kernel<T, 1><<<blocks, 256, 0, stream>>>(q, scale, static_cast<T *>(y), T_, H, ld_q, ld_y);
+    q8_dequantize_kernel<T, 1><<<blocks, 256, 0, stream>>>(q, scale, static_cast<T *>(y), T_, H, ld_q, ld_y, log2);
   return cudaGetLastError();
 }
 
@@ -319,12 +379,12 @@ cudaError_t launch_q8_rows(int dtype, const Q8RowArgs &p, int num_sms, cudaStrea
 }
 
 cudaError_t launch_q8_dequantize(int dtype, const int8_t *q, const float *scale, void *y, int64_t T, int H,
-                                 int64_t ld_q, int64_t ld_y, int num_sms, cudaStream_t stream) {
+                                 int64_t ld_q, int64_t ld_y, cudaStream_t stream) {
   if (dtype == MOE_DTYPE_BF16)
-    return launch_dequant_t<Bf16>(q, scale, y, T, H, ld_q, ld_y, num_sms, stream);
+    return launch_dequant_t<Bf16>(q, scale, y, T, H, ld_q, ld_y, stream);
   if (dtype == MOE_DTYPE_FP16)
-    return launch_dequant_t<Fp16>(q, scale, y, T, H, ld_q, ld_y, num_sms, stream);
-  return launch_dequant_t<float>(q, scale, y, T, H, ld_q, ld_y, num_sms, stream);
+    return launch_dequant_t<Fp16>(q, scale, y, T, H, ld_q, ld_y, stream);
+  return launch_dequant_t<float>(q, scale, y, T, H, ld_q, ld_y, stream);
 }
 
 }  // namespace srm

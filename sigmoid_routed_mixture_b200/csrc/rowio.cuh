@@ -64,6 +64,7 @@ constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 
 template <typename T, int E>
 struct RowIo {  // E = kVec<T>, 16-bit types
+  using Raw = uint4;  // the elements as loaded
   static __device__ __forceinline__ void unpack(const uint4 &r, float (&f)[E]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -79,6 +80,7 @@ struct RowIo {  // E = kVec<T>, 16-bit types
 };
 template <>
 struct RowIo<float, 4> {
+  using Raw = uint4;
   static __device__ __forceinline__ void unpack(const uint4 &r, float (&f)[4]) {
     f[0] = __uint_as_float(r.x);
     f[1] = __uint_as_float(r.y);
@@ -94,6 +96,8 @@ struct RowIo<float, 4> {
 };
 template <typename T>
 struct RowIo<T, 1> {
+  using Raw = T;
+  static __device__ __forceinline__ void unpack(const T &r, float (&f)[1]) { f[0] = to_float(r); }
   static __device__ __forceinline__ void load(const T *p, float (&f)[1]) { f[0] = to_float(*p); }
   static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { *p = from_float<T>(f[0]); }
 };
