@@ -162,7 +162,7 @@ cudaError_t launch_rows_sort(const RowsArgs &p, int elem, const void *x, const f
                              float *xs_scale, int num_sms, cudaStream_t stream);
 cudaError_t launch_rows_unsort(const RowsArgs &p, int dtype, int slot_dtype, const void *ys,
                                const float *gate, const int32_t *pos, const void *residual, void *y,
-                               int num_sms, cudaStream_t stream);
+                               cudaStream_t stream);
 cudaError_t launch_rows_unsort_grad(const RowsArgs &p, int dtype, int slot_dtype, const void *dy,
                                     const void *ys, const float *gate, const int32_t *pos, void *dys,
                                     float *dgate, int num_sms, cudaStream_t stream);

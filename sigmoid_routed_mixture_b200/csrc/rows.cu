@@ -5,6 +5,8 @@
 // row written once, or the reverse; the gradient of the way back reads dy once
 // for all of a token's slots.  No atomics: every output element is the work of
 // one thread, and a sum over slots or over a row runs in a fixed order.
+#include <type_traits>
+
 #include "kernels.h"
 #include "rowio.cuh"
 
@@ -70,7 +72,8 @@ __device__ __forceinline__ int row_pos(const int32_t *pos, int a, int P, int *er
   return -1;
 }
 
-constexpr int kBatch = 8;  // vectors a lane has in flight
+constexpr int kBatch = 8;              // vectors a lane has in flight
+constexpr int kSmallPositions = 4096;  // the inverse in every CTA's shared memory: 16 KB
 
 }  // namespace
 
@@ -88,14 +91,13 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The rows by token: each token row is read once and written to its positions.
-// W: the widest vector all rows are aligned to; a warp moves a part of a row.
+// The rows by token: each token row is read once and written to its positions
+// (pos: global or shared memory).  W: the widest vector all rows are aligned
+// to; a warp moves a part of a row.
 template <typename W>
-__global__ void __launch_bounds__(256)
-    rows_scatter_kernel(const RowsArgs p, const int32_t *__restrict__ pos, const uint8_t *__restrict__ x,
-                        uint8_t *__restrict__ xs, const float *__restrict__ x_scale,
-                        float *__restrict__ xs_scale, int64_t row_bytes, int64_t x_pitch, int64_t xs_pitch,
-                        int wpt) {
+__device__ __forceinline__ void scatter_tokens(const RowsArgs &p, const int32_t *pos, const uint8_t *x,
+                                               uint8_t *xs, const float *x_scale, float *xs_scale,
+                                               int64_t row_bytes, int64_t x_pitch, int64_t xs_pitch, int wpt) {
   const int lane = threadIdx.x & 31;
   const int vecs = static_cast<int>(row_bytes / sizeof(W));
   const int part = (vecs + wpt - 1) / wpt;
@@ -114,60 +116,129 @@ __global__ void __launch_bounds__(256)
     const int n_dst = p.K + p.has_shared;
     const W *src = reinterpret_cast<const W *>(x + t * x_pitch);
     for (int v0 = begin; v0 < end; v0 += 32 * kBatch) {
+      const int at = v0 + lane;
+      const bool full = v0 + 32 * kBatch <= end;  // no tests inside
       W buf[kBatch];
+      if (full) {
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (v0 + j * 32 + lane < end) buf[j] = src[v0 + j * 32 + lane];
+        for (int j = 0; j < kBatch; ++j) buf[j] = src[at + j * 32];
+      } else {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (at + j * 32 < end) buf[j] = src[at + j * 32];
+      }
       for (int k = 0; k < n_dst; ++k) {
         const int d = __shfl_sync(0xffffffffu, mine, k);
         if (d < 0) continue;
-        W *out = reinterpret_cast<W *>(xs + d * xs_pitch);
+        W *out = reinterpret_cast<W *>(xs + d * xs_pitch) + at;
+        if (full) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (v0 + j * 32 + lane < end) out[v0 + j * 32 + lane] = buf[j];
+          for (int j = 0; j < kBatch; ++j) out[j * 32] = buf[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (at + j * 32 < end) out[j * 32] = buf[j];
+        }
       }
     }
   }
 }
 
+template <typename W>
+__global__ void __launch_bounds__(256)
+    rows_scatter_kernel(const RowsArgs p, const int32_t *__restrict__ pos, const uint8_t *__restrict__ x,
+                        uint8_t *__restrict__ xs, const float *__restrict__ x_scale,
+                        float *__restrict__ xs_scale, int64_t row_bytes, int64_t x_pitch, int64_t xs_pitch,
+                        int wpt) {
+  scatter_tokens<W>(p, pos, x, xs, x_scale, xs_scale, row_bytes, x_pitch, xs_pitch, wpt);
+}
+
+// The same in one launch for few positions: every CTA builds the whole inverse
+// in its shared memory, CTA 0 writes it out, and each CTA moves its tokens.
+// (64 tokens x 9 rows of 12 KB: 8.4 us as clear, invert and scatter.)
+template <typename W>
+__global__ void __launch_bounds__(256)
+    rows_sort_small_kernel(const RowsArgs p, const int32_t *__restrict__ offsets,
+                           const int32_t *__restrict__ sorted, int32_t *__restrict__ pos,
+                           const uint8_t *__restrict__ x, uint8_t *__restrict__ xs,
+                           const float *__restrict__ x_scale, float *__restrict__ xs_scale, int64_t row_bytes,
+                           int64_t x_pitch, int64_t xs_pitch, int wpt) {
+  __shared__ int32_t inverse[kSmallPositions];
+  for (int i = threadIdx.x; i < p.P; i += 256) inverse[i] = -1;
+  __syncthreads();
+  const int n = row_total(offsets, p.E + 1, p.P, p.err);
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int a = sorted[i];
+    if (a < 0 || a >= p.P)
+      record_error(p.err, MOE_ERR_BAD_INDEX);
+    else
+      inverse[a] = i;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.P; i += 256) pos[i] = inverse[i];
+  scatter_tokens<W>(p, inverse, x, xs, x_scale, xs_scale, row_bytes, x_pitch, xs_pitch, wpt);
+}
+
 // The way back: y[t] = (residual[t] +) the weighted sum of the token's rows.
-// NB: slots and the shared row at most, all loads issued before the sums.
-template <typename Tt, typename Ts, int E, int NB>
+// 2^tpr_log2 threads share a token's row (256 >> tpr_log2 tokens a CTA); a
+// thread issues the loads of all of the token's rows before the sums.  NB:
+// slots and the shared row, at most or (kExact) exactly.  With kExact a token
+// that has all its rows takes straight-line code.
+template <typename Tt, typename Ts, int E, int NB, bool kExact>
 __global__ void __launch_bounds__(256)
     rows_unsort_kernel(const RowsArgs p, const Ts *__restrict__ ys, const float *__restrict__ gate,
-                       const int32_t *__restrict__ pos, const Tt *residual, Tt *y) {
-  const int units = (p.H + E - 1) / E;
-  const int64_t total = static_cast<int64_t>(p.T) * units;
-  const int n = p.K + p.has_shared;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int t = static_cast<int>(i / units);
-    const int c = static_cast<int>(i - static_cast<int64_t>(t) * units) * E;
-    Unit<Ts, E> v[NB];
-    int at[NB];
+                       const int32_t *__restrict__ pos, const Tt *residual, Tt *y, int tpr_log2) {
+  const int tpr = 1 << tpr_log2;
+  const int64_t t64 = (static_cast<int64_t>(blockIdx.x) << (8 - tpr_log2)) + (threadIdx.x >> tpr_log2);
+  if (t64 >= p.T) return;
+  const int t = static_cast<int>(t64);
+  const int n = kExact ? NB : p.K + p.has_shared;
+  int at[NB];
+  float g[NB];
+  bool all = true;
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      at[k] = -1;
-      if (k < n) at[k] = row_pos(pos, k < p.K ? t * p.K + k : p.T * p.K + t, p.P, p.err);
+  for (int k = 0; k < NB; ++k) {
+    at[k] = -1;
+    g[k] = 1.f;
+    if (k < n) {
+      at[k] = row_pos(pos, k < p.K ? t * p.K + k : p.T * p.K + t, p.P, p.err);
+      if (gate && k < p.K) g[k] = gate[static_cast<int64_t>(t) * p.K + k];
+      all = all && at[k] >= 0;
     }
-#pragma unroll
-    for (int k = 0; k < NB; ++k)
-      if (at[k] >= 0) v[k].load(ys + at[k] * p.ld_slot + c);
+  }
+  for (int c = (threadIdx.x & (tpr - 1)) * E; c < p.H; c += tpr * E) {
+    Unit<Ts, E> v[NB];
+    Unit<Tt, E> r;
+    if (residual) r.load(residual + t * p.ld_residual + c);
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (kExact && all) {
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      if (at[k] < 0) continue;
-      const float g = gate && k < p.K ? gate[static_cast<int64_t>(t) * p.K + k] : 1.f;
-      float f[E];
-      v[k].get(f);
+      for (int k = 0; k < NB; ++k) v[k].load(ys + at[k] * p.ld_slot + c);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(g, f[e], acc[e]);
+      for (int k = 0; k < NB; ++k) {
+        float f[E];
+        v[k].get(f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(g[k], f[e], acc[e]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        if (at[k] >= 0) v[k].load(ys + at[k] * p.ld_slot + c);
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (at[k] < 0) continue;
+        float f[E];
+        v[k].get(f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(g[k], f[e], acc[e]);
+      }
     }
     if (residual) {
-      Unit<Tt, E> r;
       float f[E];
-      r.load(residual + t * p.ld_residual + c);
       r.get(f);
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = f[e] + acc[e];
@@ -176,25 +247,26 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The gradient of the way back.  WPT warps share a token's row; dy's part
-// stays in registers while the token's slots pass.
-template <typename Tt, typename Ts, int E, int KM>
+// The gradient of the way back.  wpt warps share a token's row; a chunk of dy
+// (B units a lane) stays in registers while the token's slots pass, the next
+// slot's row already on its way.
+template <typename Tt, typename Ts, int E>
 __global__ void __launch_bounds__(256)
     rows_unsort_grad_kernel(const RowsArgs p, const Tt *__restrict__ dy, const Ts *ys,
                             const float *__restrict__ gate, const int32_t *__restrict__ pos, Ts *dys,
                             float *dgate, int wpt) {
-  constexpr int B = E == 8 && sizeof(Tt) == 4 ? kBatch / 2 : kBatch;
-  __shared__ float part[8][KM];
+  constexpr int B = 4;
+  __shared__ float partial[8][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * (8 / wpt) + warp / wpt;
+  const int64_t t64 = static_cast<int64_t>(blockIdx.x) * (8 / wpt) + warp / wpt;
+  const int t = static_cast<int>(t64);
   const int w = warp % wpt;
   const int units = (p.H + E - 1) / E;
-  const int share = (units + wpt - 1) / wpt;
+  // whole chunks to each warp, the row's ragged end to the last
+  const int share = ((units + wpt - 1) / wpt + 32 * B - 1) / (32 * B) * (32 * B);
   const int begin = min(units, w * share), end = min(units, begin + share);
-  float dot[KM];
-#pragma unroll
-  for (int k = 0; k < KM; ++k) dot[k] = 0.f;
-  if (t < p.T) {
+  float dot = 0.f;  // lane k: the k-th slot's
+  if (t64 < p.T) {
     int mine = -1;  // lane k: the token's k-th position (k <= 16)
     float my_gate = 1.f;
     if (lane < p.K) {
@@ -203,59 +275,69 @@ __global__ void __launch_bounds__(256)
     } else if (lane == p.K && p.has_shared) {
       mine = row_pos(pos, p.T * p.K + t, p.P, p.err);
     }
-    for (int u0 = begin; u0 < end; u0 += 32 * B) {
+    auto chunk = [&](int u0, auto full) {
+      constexpr bool kFull = decltype(full)::value;
+      const Tt *dy_at = dy + t * p.ld_token + (u0 + lane) * E;
+      auto inside = [&](int j) { return kFull || u0 + j * 32 + lane < end; };
       Unit<Tt, E> d[B];
 #pragma unroll
       for (int j = 0; j < B; ++j)
-        if (u0 + j * 32 + lane < end) d[j].load(dy + t * p.ld_token + (u0 + j * 32 + lane) * E);
+        if (inside(j)) d[j].load(dy_at + j * 32 * E);
+      Unit<Ts, E> v[B];
+      auto fetch = [&](int k) {
+        const int at = k < p.K ? __shfl_sync(0xffffffffu, mine, k) : -1;
+        if (!dgate || at < 0) return;
+        const Ts *src = ys + at * p.ld_slot + (u0 + lane) * E;
 #pragma unroll
-      for (int k = 0; k <= KM; ++k) {
-        if (k >= p.K + p.has_shared) break;
+        for (int j = 0; j < B; ++j)
+          if (inside(j)) v[j].load(src + j * 32 * E);
+      };
+      fetch(0);
+      for (int k = 0; k < p.K + p.has_shared; ++k) {
         const int at = __shfl_sync(0xffffffffu, mine, k);
         const float g = __shfl_sync(0xffffffffu, my_gate, k);
-        if (at < 0) continue;
-        if (dgate && k < p.K) {
-          Unit<Ts, E> v[B];
+        float s = 0.f;
+        if (dgate && k < p.K && at >= 0) {
 #pragma unroll
           for (int j = 0; j < B; ++j)
-            if (u0 + j * 32 + lane < end) v[j].load(ys + at * p.ld_slot + (u0 + j * 32 + lane) * E);
-          float s = 0.f;
-#pragma unroll
-          for (int j = 0; j < B; ++j)
-            if (u0 + j * 32 + lane < end) {
+            if (inside(j)) {
               float a[E], b[E];
               d[j].get(a);
               v[j].get(b);
 #pragma unroll
               for (int e = 0; e < E; ++e) s = fmaf(a[e], b[e], s);
             }
-          if (k < KM) dot[k < KM ? k : 0] += s;
         }
-        if (dys) {
+        if (k + 1 < p.K) fetch(k + 1);
+        if (dgate && k < p.K) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (lane == k) dot += s;
+        }
+        if (dys && at >= 0) {
+          Ts *dst = dys + at * p.ld_dys + (u0 + lane) * E;
 #pragma unroll
           for (int j = 0; j < B; ++j)
-            if (u0 + j * 32 + lane < end) {
+            if (inside(j)) {
               float a[E];
               d[j].get(a);
 #pragma unroll
               for (int e = 0; e < E; ++e) a[e] *= g;
-              Unit<Ts, E>::store(dys + at * p.ld_dys + (u0 + j * 32 + lane) * E, a);
+              Unit<Ts, E>::store(dst + j * 32 * E, a);
             }
         }
       }
-    }
+    };
+    int u0 = begin;
+    for (; u0 + 32 * B <= end; u0 += 32 * B) chunk(u0, std::true_type{});
+    if (u0 < end) chunk(u0, std::false_type{});
   }
   if (!dgate) return;
-#pragma unroll
-  for (int k = 0; k < KM; ++k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], o);
-    if (lane == 0) part[warp][k] = dot[k];
-  }
+  if (lane < p.K) partial[warp][lane] = dot;
   __syncthreads();
-  if (t < p.T && w == 0 && lane < p.K) {
+  if (t64 < p.T && w == 0 && lane < p.K) {
     float s = 0.f;
-    for (int j = 0; j < wpt; ++j) s += part[warp + j][lane];
+    for (int j = 0; j < wpt; ++j) s += partial[warp + j][lane];
     dgate[static_cast<int64_t>(t) * p.K + lane] = s;
   }
 }
@@ -266,36 +348,65 @@ bool is_aligned(const void *p, int64_t pitch_bytes, int a) {
   return !p || (reinterpret_cast<uintptr_t>(p) % a == 0 && pitch_bytes % a == 0);
 }
 
+struct SortPtrs {
+  const void *x;
+  const float *x_scale;
+  const int32_t *offsets, *sorted;
+  int32_t *pos;
+  void *xs;
+  float *xs_scale;
+};
+
 template <typename W>
-cudaError_t launch_scatter(const RowsArgs &p, const int32_t *pos, const void *x, void *xs,
-                           const float *x_scale, float *xs_scale, int elem, int num_sms,
-                           cudaStream_t stream) {
+cudaError_t launch_sort_w(const RowsArgs &p, const SortPtrs &a, int elem, int num_sms, cudaStream_t stream) {
   int wpt = 1;  // warps per token: at least ~32 warps per SM in flight
   while (wpt < 8 && static_cast<int64_t>(p.T) * wpt < num_sms * 32) wpt *= 2;
   const int64_t blocks = (static_cast<int64_t>(p.T) * wpt + 7) / 8, cap = num_sms * 16ll;
-  rows_scatter_kernel<W><<<static_cast<unsigned>(blocks < cap ? blocks : cap), 256, 0, stream>>>(
-      p, pos, static_cast<const uint8_t *>(x), static_cast<uint8_t *>(xs), x_scale, xs_scale,
-      static_cast<int64_t>(p.H) * elem, p.ld_token * elem, p.ld_slot * elem, wpt);
+  const unsigned grid = static_cast<unsigned>(blocks < cap ? blocks : cap);
+  const uint8_t *x = static_cast<const uint8_t *>(a.x);
+  uint8_t *xs = static_cast<uint8_t *>(a.xs);
+  const int64_t row = static_cast<int64_t>(p.H) * elem;
+  if (p.P <= kSmallPositions) {
+    rows_sort_small_kernel<W><<<grid, 256, 0, stream>>>(p, a.offsets, a.sorted, a.pos, x, xs, a.x_scale,
+                                                        a.xs_scale, row, p.ld_token * elem, p.ld_slot * elem, wpt);
+    return cudaGetLastError();
+  }
+  cudaError_t e = cudaMemsetAsync(a.pos, 0xff, sizeof(int32_t) * static_cast<size_t>(p.P), stream);
+  if (e != cudaSuccess) return e;
+  const int64_t inv = (p.P + 255ll) / 256, inv_cap = num_sms * 8ll;
+  rows_invert_kernel<<<static_cast<unsigned>(inv < inv_cap ? inv : inv_cap), 256, 0, stream>>>(p, a.offsets,
+                                                                                              a.sorted, a.pos);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  rows_scatter_kernel<W><<<grid, 256, 0, stream>>>(p, a.pos, x, xs, a.x_scale, a.xs_scale, row,
+                                                   p.ld_token * elem, p.ld_slot * elem, wpt);
   return cudaGetLastError();
 }
 
 template <typename Tt, typename Ts, int E>
 cudaError_t launch_unsort_e(const RowsArgs &p, const void *ys, const float *gate, const int32_t *pos,
-                            const void *residual, void *y, int num_sms, cudaStream_t stream) {
-  const int64_t total = static_cast<int64_t>(p.T) * ((p.H + E - 1) / E);
-  const int64_t blocks = (total + 255) / 256, cap = num_sms * 32ll;
-  const unsigned grid = static_cast<unsigned>(blocks < cap ? blocks : cap);
+                            const void *residual, void *y, cudaStream_t stream) {
+  const int units = (p.H + E - 1) / E;
+  int log2 = 0;  // threads per token
+  while (log2 < 8 && (1 << log2) < units) ++log2;
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.T) + (256 >> log2) - 1) >> (8 - log2));
   auto go = [&](auto kern) {
     kern<<<grid, 256, 0, stream>>>(p, static_cast<const Ts *>(ys), gate, pos,
-                                   static_cast<const Tt *>(residual), static_cast<Tt *>(y));
+                                   static_cast<const Tt *>(residual), static_cast<Tt *>(y), log2);
   };
   const int n = p.K + p.has_shared;
-  if (n <= 5)
-    go(rows_unsort_kernel<Tt, Ts, E, 5>);
-  else if (n <= 9)
-    go(rows_unsort_kernel<Tt, Ts, E, 9>);
+  if (n == 4)
+    go(rows_unsort_kernel<Tt, Ts, E, 4, true>);
+  else if (n == 5)
+    go(rows_unsort_kernel<Tt, Ts, E, 5, true>);
+  else if (n == 8)
+    go(rows_unsort_kernel<Tt, Ts, E, 8, true>);
+  else if (n == 9)
+    go(rows_unsort_kernel<Tt, Ts, E, 9, true>);
+  else if (n < 8)
+    go(rows_unsort_kernel<Tt, Ts, E, 7, false>);
   else
-    go(rows_unsort_kernel<Tt, Ts, E, 17>);
+    go(rows_unsort_kernel<Tt, Ts, E, 17, false>);
   return cudaGetLastError();
 }
 
@@ -304,17 +415,9 @@ cudaError_t launch_grad_e(const RowsArgs &p, const void *dy, const void *ys, con
                           const int32_t *pos, void *dys, float *dgate, int num_sms, cudaStream_t stream) {
   int wpt = 1;
   while (wpt < 8 && static_cast<int64_t>(p.T) * wpt < num_sms * 32) wpt *= 2;
-  const unsigned grid = static_cast<unsigned>((p.T + 8 / wpt - 1) / (8 / wpt));
-  auto go = [&](auto kern) {
-    kern<<<grid, 256, 0, stream>>>(p, static_cast<const Tt *>(dy), static_cast<const Ts *>(ys), gate, pos,
-                                   static_cast<Ts *>(dys), dgate, wpt);
-  };
-  if (p.K <= 4)
-    go(rows_unsort_grad_kernel<Tt, Ts, E, 4>);
-  else if (p.K <= 8)
-    go(rows_unsort_grad_kernel<Tt, Ts, E, 8>);
-  else
-    go(rows_unsort_grad_kernel<Tt, Ts, E, 16>);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.T) + 8 / wpt - 1) / (8 / wpt));
+  rows_unsort_grad_kernel<Tt, Ts, E><<<grid, 256, 0, stream>>>(
+      p, static_cast<const Tt *>(dy), static_cast<const Ts *>(ys), gate, pos, static_cast<Ts *>(dys), dgate, wpt);
   return cudaGetLastError();
 }
 
@@ -336,35 +439,29 @@ cudaError_t by_types(int tok, int slot, F f) {
 cudaError_t launch_rows_sort(const RowsArgs &p, int elem, const void *x, const float *x_scale,
                              const int32_t *offsets, const int32_t *sorted, int32_t *pos, void *xs,
                              float *xs_scale, int num_sms, cudaStream_t stream) {
-  cudaError_t e = cudaMemsetAsync(pos, 0xff, sizeof(int32_t) * static_cast<size_t>(p.P), stream);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = (p.P + 255ll) / 256, cap = num_sms * 8ll;
-  rows_invert_kernel<<<static_cast<unsigned>(blocks < cap ? blocks : cap), 256, 0, stream>>>(p, offsets,
-                                                                                            sorted, pos);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   const int64_t row = static_cast<int64_t>(p.H) * elem;
-  auto fits = [&](int a) {
-    return row % a == 0 && is_aligned(x, p.ld_token * elem, a) && is_aligned(xs, p.ld_slot * elem, a);
+  const SortPtrs a = {x, x_scale, offsets, sorted, pos, xs, xs_scale};
+  auto fits = [&](int n) {
+    return row % n == 0 && is_aligned(x, p.ld_token * elem, n) && is_aligned(xs, p.ld_slot * elem, n);
   };
-  if (fits(16)) return launch_scatter<uint4>(p, pos, x, xs, x_scale, xs_scale, elem, num_sms, stream);
-  if (fits(8)) return launch_scatter<uint2>(p, pos, x, xs, x_scale, xs_scale, elem, num_sms, stream);
-  if (fits(4)) return launch_scatter<uint32_t>(p, pos, x, xs, x_scale, xs_scale, elem, num_sms, stream);
-  if (fits(2)) return launch_scatter<uint16_t>(p, pos, x, xs, x_scale, xs_scale, elem, num_sms, stream);
-  return launch_scatter<uint8_t>(p, pos, x, xs, x_scale, xs_scale, elem, num_sms, stream);
+  if (fits(16)) return launch_sort_w<uint4>(p, a, elem, num_sms, stream);
+  if (fits(8)) return launch_sort_w<uint2>(p, a, elem, num_sms, stream);
+  if (fits(4)) return launch_sort_w<uint32_t>(p, a, elem, num_sms, stream);
+  if (fits(2)) return launch_sort_w<uint16_t>(p, a, elem, num_sms, stream);
+  return launch_sort_w<uint8_t>(p, a, elem, num_sms, stream);
 }
 
 cudaError_t launch_rows_unsort(const RowsArgs &p, int dtype, int slot_dtype, const void *ys,
                                const float *gate, const int32_t *pos, const void *residual, void *y,
-                               int num_sms, cudaStream_t stream) {
+                               cudaStream_t stream) {
   return by_types(dtype, slot_dtype, [&](auto tt, auto ts) {
     using Tt = decltype(tt);
     using Ts = decltype(ts);
     const int64_t a = sizeof(Tt), b = sizeof(Ts);
     if (p.H % 8 == 0 && is_aligned(ys, p.ld_slot * b, 16) && is_aligned(residual, p.ld_residual * a, 16) &&
         is_aligned(y, p.ld_token * a, 16))
-      return launch_unsort_e<Tt, Ts, 8>(p, ys, gate, pos, residual, y, num_sms, stream);
-    return launch_unsort_e<Tt, Ts, 1>(p, ys, gate, pos, residual, y, num_sms, stream);
+      return launch_unsort_e<Tt, Ts, 8>(p, ys, gate, pos, residual, y, stream);
+    return launch_unsort_e<Tt, Ts, 1>(p, ys, gate, pos, residual, y, stream);
   });
 }
 

@@ -82,7 +82,7 @@ moe_status_t moe_rows_unsort(const moe_rows_cfg_t *cfg, const void *ys, const fl
       (residual && !aligned(residual, e)) || !aligned(y, e) || !aligned(ws, 256))
     return MOE_ERR_ALIGN;
   return cuda_status(srm::launch_rows_unsort(args(*cfg, ws), cfg->dtype, cfg->slot_dtype, ys, gate, pos,
-                                             residual, y, num_sms(), static_cast<cudaStream_t>(stream)));
+                                             residual, y, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_rows_sort_grad(const moe_rows_cfg_t *cfg, const void *dxs, const int32_t *pos, void *dx,
