@@ -192,9 +192,10 @@ struct Q8GemmArgs {
 struct Q8Plan {
   bool pair, streamed;
   int units;
-  int64_t max_mtiles, partials;  // partial sums in int32
+  int64_t max_mtiles;
 };
 Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms);
+int64_t q8_partials(int64_t R, int num_sms);  // int32 partial sums in the workspace
 cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const TokMaps &tok, const CUtensorMap &tw,
                            const Q8GemmArgs &p, int num_sms, cudaStream_t stream);
 

@@ -91,8 +91,8 @@ size_t control_bytes() {
   // pairs (half as many units), 4 for single CTAs
   return kPartCounters + sizeof(unsigned) * 8 * static_cast<size_t>((num_sms() + 31) / 32 * 32);
 }
-size_t matmul_ws_bytes(const srm::Q8Plan &p) {
-  return control_bytes() + sizeof(int32_t) * static_cast<size_t>(p.partials);
+size_t matmul_ws_bytes(int64_t R) {
+  return control_bytes() + sizeof(int32_t) * static_cast<size_t>(srm::q8_partials(R, num_sms()));
 }
 
 }  // namespace
@@ -101,7 +101,7 @@ extern "C" {
 
 size_t moe_q8_matmul_workspace_size(const moe_q8_matmul_t *cfg) {
   if (check_matmul(cfg) != MOE_OK) return 0;
-  return matmul_ws_bytes(srm::q8_plan(cfg->R, cfg->N, cfg->K, cfg->groups, num_sms()));
+  return matmul_ws_bytes(cfg->R);
 }
 
 moe_status_t moe_q8_workspace_init(void *ws, size_t ws_bytes, void *stream) {
@@ -133,7 +133,7 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
       !aligned(y, e) || !aligned(ws, 256))
     return MOE_ERR_ALIGN;
   const srm::Q8Plan plan = srm::q8_plan(cfg->R, cfg->N, cfg->K, cfg->groups, num_sms());
-  if (ws_bytes < matmul_ws_bytes(plan)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < matmul_ws_bytes(cfg->R)) return MOE_ERR_WORKSPACE;
   uint8_t *wsb = static_cast<uint8_t *>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   srm::TokMaps tok;

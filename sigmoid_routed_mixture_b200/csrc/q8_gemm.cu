@@ -817,8 +817,14 @@ Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms) {
     while ((parts + 1) * parts * cost <= kblocks && (parts + 1) * tiles <= units) ++parts;
     p.units = static_cast<int>(parts * tiles);
   }
-  p.partials = p.streamed ? static_cast<int64_t>(p.units) * 2 * (p.pair ? 2 : 1) * bt * 128 : 0;
   return p;
+}
+
+// Two parts of a tile per unit, whatever the other sizes: a workspace for some
+// rows serves every product of no more rows.
+int64_t q8_partials(int64_t R, int num_sms) {
+  return R <= kQ8SoloRows ? int64_t(num_sms) * 2 * kQ8SoloRows * 128
+                          : int64_t(num_sms / 2) * 2 * 2 * kQ8PairRows * 128;
 }
 
 }  // namespace srm

@@ -237,3 +237,128 @@ def matmul(cfg: MatmulConfig, x, x_scale, w, w_scale, ws, offsets=None, residual
     if rc:
         raise moe.MoeError(rc, "moe_q8_matmul")
     return out
+
+
+# ------------------------------------------------------------------ blocks
+
+class MoeBlock:
+    """One MoE block in 8 bits: ``y = block(x)``, the 8-bit form of moe.MoeBlock (same arguments).
+
+    Router and selection are the bf16 block's; the experts' products take 8-bit rows and weights, the
+    rows go to the experts in 8 bits (half the bytes) and come back with the gates applied by the row
+    calls.  Its buffers belong to the block: one call at a time, and y holds until the next."""
+
+    def __init__(self, cfg: moe.Config, w_router, bias, w1, w3, w2, ws1=None, ws3=None, ws2=None, packed=None):
+        from . import ep, rows  # rows shares this module's marshalling
+        self._rows = rows
+        self.cfg, self.w_router, self.bias = cfg, w_router, bias
+        # packed: pack_weights' result for this block's H, I and E, shared with another block
+        self.weights = packed if packed is not None else pack_weights(cfg, w1, w3, w2, ws1, ws3, ws2)
+        self.router_packed = moe.pack_router(cfg, w_router)
+        dev, T, K, E, H, I, P = w_router.device, cfg.T, cfg.K, cfg.E, cfg.H, cfg.I, cfg.rows
+        self.ws = moe.workspace(cfg, device=dev)
+        G = E + int(bool(cfg.has_shared))
+        self.up = MatmulConfig(P, 2 * I, H, groups=G, swiglu=True, dtype=torch.float16)
+        self.down = MatmulConfig(P, H, I, groups=G, dtype=torch.float16)
+        self.mm_ws = workspace(self.up, self.down, device=dev)
+        self.there = rows.Config.of(cfg, dtype=torch.int8)
+        self.back = rows.Config.of(cfg)
+        self.idx = torch.empty((T, K), dtype=torch.int32, device=dev)
+        self.gate = torch.empty((T, K), dtype=torch.float32, device=dev)
+        self.margin = torch.empty((T,), dtype=torch.float32, device=dev)
+        self.counts = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+        self.offsets = torch.empty((E + 2,), dtype=torch.int32, device=dev)
+        self.sorted = torch.empty((P,), dtype=torch.int32, device=dev)
+        self.pos = torch.empty((P,), dtype=torch.int32, device=dev)
+        self.q = (torch.empty((T, H), dtype=torch.int8, device=dev), torch.empty((T,), dtype=torch.float32, device=dev))
+        # the sorted rows and the experts' outputs use the places the bf16 block's workspace has for them
+        at = ep.workspace_offset(cfg, ep.WS_TOKEN_ROWS) if T else 0
+        self.xs = self.ws[at:at + P * H].view(torch.int8).view(P, H)
+        self.xs_scale = torch.empty((P,), dtype=torch.float32, device=dev)
+        self.h = torch.empty((P, I), dtype=torch.float16, device=dev)
+        self.hq = (torch.empty((P, I), dtype=torch.int8, device=dev), torch.empty((P,), dtype=torch.float32, device=dev))
+        at = ep.workspace_offset(cfg, ep.WS_SLOT_OUTPUTS) if T else 0
+        self.ys = self.ws[at:at + 2 * P * H].view(torch.float16).view(P, H)
+        self.y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+
+    def _run(self, x_ffn, residual, logits):
+        w13, w13_scale, w2, w2_scale = self.weights
+        rows = self._rows
+        moe.route_packed(self.cfg, x_ffn, self.router_packed, self.bias, self.ws,
+                         out=(self.idx, self.gate, self.margin), logits=logits)
+        moe.permute(self.cfg, self.idx, self.ws, out=(self.counts, self.offsets, self.sorted))
+        rows.sort(self.there, self.q[0], self.offsets, self.sorted, self.ws, x_scale=self.q[1], out=self.xs,
+                  pos=self.pos, xs_scale=self.xs_scale)
+        matmul(self.up, self.xs, self.xs_scale, w13, w13_scale, self.mm_ws, offsets=self.offsets, out=self.h)
+        quantize(self.h, out=self.hq)
+        matmul(self.down, self.hq[0], self.hq[1], w2, w2_scale, self.mm_ws, offsets=self.offsets, out=self.ys)
+        return rows.unsort(self.back, self.ys, self.gate, self.pos, self.ws, residual=residual, out=self.y)
+
+    def sublayer(self, x_resid, gamma, eps=1e-5, stream=None, logits=None, delta=None):
+        """The decoder block's FFN sublayer: x' + MoE(RMSNorm(x')) and the normalised rows, with
+        x' = x_resid + delta in one pass where the previous sublayer's output ``delta`` is given."""
+        if elsewhere(x_resid, stream):
+            with on(x_resid, stream):
+                return self.sublayer(x_resid, gamma, eps, None, logits, delta)
+        x_ffn = torch.empty_like(x_resid)
+        x_sum = x_resid if delta is None else torch.empty_like(x_resid)
+        add_rmsnorm(x_resid, gamma, eps, delta=delta, x_out=None if delta is None else x_sum, y=x_ffn, out=self.q)
+        return self._run(x_ffn, x_sum, logits), x_ffn
+
+    def __call__(self, x, stream=None, logits=None):
+        if elsewhere(x, stream):
+            with on(x, stream):
+                return self(x, None, logits)
+        quantize(x, out=self.q)
+        return self._run(x, None, logits)
+
+    def device_error(self, stream=None) -> int:
+        """Read and clear the block's device error words (synchronises the stream)."""
+        first, second = moe.device_error(self.ws, stream), moe.device_error(self.mm_ws, stream)
+        return first or second
+
+
+class DenseMlp:
+    """A dense SwiGLU MLP in 8 bits (the 8-bit form of moe.dense_mlp): ``y = mlp(x)`` for up to cfg.T
+    rows, cfg from moe.Config.dense; w1, w3: bf16 [I, H], w2: bf16 [H, I]."""
+
+    def __init__(self, cfg: moe.Config, w1, w3, w2, packed=None):
+        if cfg.E != 0 or cfg.K != 0 or not cfg.has_shared:
+            raise ValueError("DenseMlp takes a moe.Config.dense configuration")
+        self.cfg, self.dev = cfg, (packed[0] if packed is not None else w1).device
+        self.weights = packed if packed is not None else pack_weights(cfg, None, None, None, w1, w3, w2)
+        self.ws = workspace(*self._shapes(cfg.T), device=self.dev)
+
+    def _shapes(self, R):
+        H, I = self.cfg.H, self.cfg.I
+        return MatmulConfig(R, 2 * I, H, swiglu=True, dtype=torch.float16), MatmulConfig(R, H, I)
+
+    def __call__(self, x, residual=None, out=None, stream=None):
+        """(residual +) W2 (silu(W1 x) * W3 x): bf16 [R, H], R <= cfg.T."""
+        if elsewhere(x, stream):
+            with on(x, stream):
+                return self(x, residual, out)
+        return self._mlp(quantize(x), residual, out)
+
+    def sublayer(self, x_resid, gamma, eps=1e-5, delta=None, stream=None):
+        """x' + MLP(RMSNorm(x')), x' = x_resid (+ delta)."""
+        if elsewhere(x_resid, stream):
+            with on(x_resid, stream):
+                return self.sublayer(x_resid, gamma, eps, delta)
+        x_sum = x_resid if delta is None else torch.empty_like(x_resid)
+        q = add_rmsnorm(x_resid, gamma, eps, delta=delta, x_out=None if delta is None else x_sum)
+        return self._mlp(q, x_sum, None)
+
+    def _mlp(self, q, residual, out):
+        w13, w13_scale, w2, w2_scale = self.weights
+        R = q[0].shape[0]
+        if R > self.cfg.T:
+            raise ValueError("%d rows, the MLP was made for %d" % (R, self.cfg.T))
+        up, down = self._shapes(R)
+        h = matmul(up, q[0], q[1], w13, w13_scale, self.ws)
+        hq, h_scale = quantize(h)
+        return matmul(down, hq, h_scale, w2, w2_scale, self.ws, residual=residual, out=out)
+
+    def device_error(self, stream=None) -> int:
+        """Read and clear the device error word (synchronises the stream)."""
+        return moe.device_error(self.ws, stream)
