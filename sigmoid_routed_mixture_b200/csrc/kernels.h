@@ -170,6 +170,7 @@ cudaError_t launch_rows_unsort_grad(const RowsArgs &p, int dtype, int slot_dtype
 // ---- products of 8-bit integers (q8_gemm.cu)
 constexpr int kQ8MaxGroups = 257;
 constexpr int kQ8PairRows = 256, kQ8SoloRows = 64;  // token rows per tile
+constexpr int kQ8EpiWarps = 8;  // epilogue warps of a CTA, two per lane quarter of tensor memory
 constexpr int kQ8Ready = 0x5a5a5a5a;
 struct Q8GemmArgs {
   const float *x_scale;    // [R]
@@ -181,7 +182,7 @@ struct Q8GemmArgs {
   int *err;
   int *ready;              // kQ8Ready while the counters below are zero between calls
   unsigned *tile_counter;
-  unsigned *part_counter;  // streamed: [tiles][CTAs of a unit][4 warps]
+  unsigned *part_counter;  // streamed: [tiles][CTAs of a unit][epilogue warps]
   int32_t *partial;        // streamed: [units][2][CTAs of a unit][token column][128]
   int R, N, K, groups;
   int streamed;            // the tiles' k-blocks in equal shares (few tiles), or whole tiles

@@ -87,9 +87,9 @@ moe_status_t check_matmul(const moe_q8_matmul_t *c) {
 // serves products of several shapes in turn.
 constexpr size_t kReadyOffset = 128, kPartCounters = 256;
 size_t control_bytes() {
-  // streamed work has fewer than two tiles per unit: 8 counters a tile for
-  // pairs (half as many units), 4 for single CTAs
-  return kPartCounters + sizeof(unsigned) * 8 * static_cast<size_t>((num_sms() + 31) / 32 * 32);
+  // streamed work has fewer than two tiles per unit (a CTA, or a pair), and a
+  // counter for each epilogue warp of a tile
+  return kPartCounters + sizeof(unsigned) * 2 * srm::kQ8EpiWarps * static_cast<size_t>((num_sms() + 31) / 32 * 32);
 }
 size_t matmul_ws_bytes(int64_t R) {
   return control_bytes() + sizeof(int32_t) * static_cast<size_t>(srm::q8_partials(R, num_sms()));

@@ -40,7 +40,7 @@ constexpr int BM = 128;           // weight rows per CTA (tensor-memory lanes)
 constexpr int BK = 128;           // elements (bytes) of K per step: one swizzle atom
 constexpr int TOK_BOX = 32;       // token rows per TMA box of a tail tile
 constexpr int TOK_BOX_BIG = 128;  // ... of a full tile
-constexpr int EPI_WARPS = 4;
+constexpr int EPI_WARPS = kQ8EpiWarps;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int MAX_GROUPS = kQ8MaxGroups;
 constexpr int MAX_STAGES = 8;
@@ -65,7 +65,7 @@ struct Smem {
   uint64_t empty[MAX_STAGES];
   uint64_t tile_full[TILE_RING];
   uint64_t tile_empty[TILE_RING];
-  int tile_ring[TILE_RING];
+  alignas(16) int tile_ring[TILE_RING][4];  // g (-1: no more), first row, rows, first weight row
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
@@ -141,7 +141,8 @@ __device__ __forceinline__ Tile decode(const Smem &s, const Q8GemmArgs &p, int n
   }
   const int mblocks = s.tile_start[lo + 1] - s.tile_start[lo];
   const int local = c.id - s.tile_start[lo] * n_tiles;
-  const int m0 = static_cast<int>(local / (static_cast<int64_t>(m_chunk) * n_tiles)) * m_chunk;
+  // (a group of at most m_chunk token blocks, the usual one, needs no division)
+  const int m0 = mblocks <= m_chunk ? 0 : local / n_tiles / m_chunk * m_chunk;
   const int cm = min(m_chunk, mblocks - m0);  // token blocks in this chunk
   const int r = local - m0 * n_tiles;
   const int nt = r / cm;
@@ -153,6 +154,20 @@ __device__ __forceinline__ Tile decode(const Smem &s, const Q8GemmArgs &p, int n
   c.n = max(32, (c.rows + 31) & ~31);
   c.w0 = nt * Cfg<kPair>::W_BLOCK;
   return c;
+}
+
+// The tile that the scheduler published in ring slot ts; false: no more.
+__device__ __forceinline__ bool ring_tile(const Smem &s, uint32_t ts, int kblocks, Tile *c) {
+  const volatile int *e = s.tile_ring[ts];
+  c->g = e[0];
+  c->row_base = e[1];
+  c->rows = e[2];
+  c->w0 = e[3];
+  c->n = max(32, (c->rows + 31) & ~31);
+  c->id = 0;  // only parts of streamed tiles are counted
+  c->kb0 = 0;
+  c->kb1 = kblocks;
+  return c->g >= 0;
 }
 
 // A unit's share of the streamed k-blocks: [begin(u), begin(u + 1)) of
@@ -186,18 +201,17 @@ struct Stream {
   }
 };
 
-// Results to their type: fp16 saturates at +-65504 (flagged), as the library's
-// other fp16 intermediates do; NaN stays NaN.
+// Results to their type: fp16 saturates at +-65504 (flagged at the end by the
+// largest magnitude seen), as the library's other fp16 intermediates do; NaN
+// stays NaN.
 template <typename T>
-__device__ __forceinline__ float fit(float v, bool &sat) {
+__device__ __forceinline__ float fit(float v, float &largest) {
   return v;
 }
 template <>
-__device__ __forceinline__ float fit<Fp16>(float v, bool &sat) {
-  if (fabsf(v) > 65504.f) {
-    sat = true;
-    v = copysignf(65504.f, v);
-  }
+__device__ __forceinline__ float fit<Fp16>(float v, float &largest) {
+  largest = fmaxf(largest, fabsf(v));
+  asm("max.NaN.f32 %0, %0, 0fC77FE000;\n\tmin.NaN.f32 %0, %0, 0f477FE000;" : "+f"(v));
   return v;
 }
 
@@ -339,20 +353,28 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
     // without work, and 24 with two tiles, at 144 tiles.)
     uint32_t stage = 0, phase = 0, ts = 0, tph = 0;
     uint32_t ps = 0, pph = 0;  // next ring slot to publish and its phase
+    const int stride = static_cast<int>(gridDim.x) / C::RANKS;
     int last = static_cast<int>(blockIdx.x) / C::RANKS;  // the newest tile of this unit
     auto publish = [&](bool draw) {
       if (!mbar_wait(&s.tile_empty[ps], pph ^ 1u, abort_flag, p.err)) return false;
       if (lane == 0) {
-        const int stride = static_cast<int>(gridDim.x) / C::RANKS;
         int t = last;
         if (draw)  // as many draws as tiles: the last one leaves the counter at 0
           t = counted ? static_cast<int>(atomicInc(p.tile_counter, total_tiles - 1)) + stride : last + stride;
         last = t;
-        if (t >= total_tiles) t = -1;
-        s.tile_ring[ps] = t;
+        // the other roles (and the peer) get the tile's place worked out
+        Tile c;
+        c.g = -1;
+        c.row_base = c.rows = c.w0 = 0;
+        if (t < total_tiles) c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, t);
+        *reinterpret_cast<int4 *>(s.tile_ring[ps]) = make_int4(c.g, c.row_base, c.rows, c.w0);
         mbar_arrive(&s.tile_full[ps]);
         if (kPair) {
-          st_shared_remote(cluster_map(&s.tile_ring[ps], 1), t);
+          const uint32_t peer = cluster_map(s.tile_ring[ps], 1);
+          st_shared_remote(peer, c.g);
+          st_shared_remote(peer + 4, c.row_base);
+          st_shared_remote(peer + 8, c.rows);
+          st_shared_remote(peer + 12, c.w0);
           mbar_arrive_remote(cluster_map(&s.tile_full[ps], 1));
         }
       }
@@ -370,13 +392,12 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
         if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
       } else {
         if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
-        const int tile = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+        const bool any_left = ring_tile(s, ts, kblocks, &c);
         if (++ts == TILE_RING) {
           ts = 0;
           tph ^= 1u;
         }
-        if (tile < 0) break;
-        c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, tile);
+        if (!any_left) break;
       }
       const int w_row = c.g * p.N + c.w0 + static_cast<int>(rank) * BM;
       const int tok_rows = kPair ? c.n / 2 : c.n;
@@ -431,13 +452,12 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
           if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
         } else {
           if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err)) break;
-          const int tile = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+          const bool any_left = ring_tile(s, ts, kblocks, &c);
           if (++ts == TILE_RING) {
             ts = 0;
             tph ^= 1u;
           }
-          if (tile < 0) break;
-          c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, tile);
+          if (!any_left) break;
         }
         const uint32_t idesc = idesc_i8(C::W_BLOCK, c.n);
         if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
@@ -492,7 +512,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
     // ------------------------------------------------------------ epilogue
     // Warp q = warp % 4 reads tensor-memory lanes 32q .. 32q+31: one weight
     // row (channel) a lane, the tile's token rows along the columns.
+    // The warps of a lane quarter take its 32-column chunks in turn.
     const int q = warp & 3;
+    constexpr int STEP = EPI_WARPS / 4;
+    const int m_first = (warp - 2) / 4;
     uint32_t acc = 0, acc_phase = 0, ts = 0, tph = 0;
     float *row_scale = s.row_scale[warp - 2];
     while (true) {
@@ -502,13 +525,12 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
         if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
       } else {
         if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
-        const int tile = *reinterpret_cast<volatile int *>(&s.tile_ring[ts]);
+        const bool any_left = ring_tile(s, ts, kblocks, &c);
         if (++ts == TILE_RING) {
           ts = 0;
           tph ^= 1u;
         }
-        if (tile < 0) break;
-        c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, tile);
+        if (!any_left) break;
       }
       const int wr = c.w0 + static_cast<int>(rank) * BM + q * 32;  // this warp's first channel
       const float ws = wr + lane < p.N ? p.w_scale[static_cast<int64_t>(c.g) * p.N + wr + lane] : 0.f;
@@ -534,12 +556,12 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
           }
         }
       };
-      const bool add = !kSwiglu && p.residual && inside;
-      if (add) load_residual(0);
+      const bool any = wr < p.N && 32 * m_first < c.n;  // something to do for this warp
+      const bool add = !kSwiglu && p.residual && inside && 32 * m_first < c.rows;
+      if (add) load_residual(m_first);
       if (!mbar_wait(&s.tfull[acc], acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + acc * BT + (static_cast<uint32_t>(q * 32) << 16);
-      const bool any = wr < p.N;
       const bool part = c.kb1 - c.kb0 < kblocks;
       bool mine = any;
       // a part's sums: [unit][its first or another part][CTA][column][lane]
@@ -555,7 +577,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
         first_unit = stream.unit_of(tile0);
         last_unit = stream.unit_of(tile0 + kblocks - 1);
         int32_t *dst = slab(unit);
-        for (int m = 0; 32 * m < c.n; ++m) {
+        for (int m = m_first; 32 * m < c.n; m += STEP) {
           uint32_t cv[32];
           tmem_ld32(taddr + 32 * m, cv);
           tmem_ld_wait();
@@ -567,13 +589,13 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
         int seen = 0;
         if (lane == 0)
           seen = static_cast<int>(
-              atomicInc(p.part_counter + (c.id * C::RANKS + rank) * 4 + q, last_unit - first_unit));
+              atomicInc(p.part_counter + (c.id * C::RANKS + rank) * EPI_WARPS + warp - 2, last_unit - first_unit));
         mine = __shfl_sync(0xffffffffu, seen, 0) == last_unit - first_unit;
         __threadfence();
       }
-      bool sat = false;
+      float largest = 0.f;
       if (mine) {
-        for (int m = 0; 32 * m < c.n; ++m) {
+        for (int m = m_first; 32 * m < c.n; m += STEP) {
           const int64_t row0 = c.row_base + 32 * m;
           const int live = min(32, c.rows - 32 * m);  // rows of the chunk
           // A store covers one row's 32 channels (SwiGLU: two rows' 16
@@ -610,7 +632,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
               const float got = __shfl_xor_sync(0xffffffffu, high ? v[k] : v[k + 1], 16);
               const float gate = high ? got : v[k], up = high ? v[k + 1] : got;
               const float h = silu<T>(gate) * up;
-              out[k / 2] = from_float<T>(fit<T>(h, sat));
+              out[k / 2] = from_float<T>(fit<T>(h, largest));
             }
             if (live == 32) {
 #pragma unroll
@@ -630,23 +652,23 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
                 for (int k = 0; k < 32; ++k)
                   if (k < live) v[k] += to_float(res[kSwiglu ? 0 : k]);
               }
-              if (32 * (m + 1) < c.rows) load_residual(m + 1);
+              if (32 * (m + STEP) < c.rows) load_residual(m + STEP);
             }
             T *y = static_cast<T *>(p.y) + row0 * p.ld_y + ch;
             if (live == 32) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k, y += p.ld_y) *y = from_float<T>(fit<T>(v[k], sat));
+              for (int k = 0; k < 32; ++k, y += p.ld_y) *y = from_float<T>(fit<T>(v[k], largest));
             } else {
 #pragma unroll
               for (int k = 0; k < 32; ++k, y += p.ld_y) {
                 if (k >= live) break;
-                *y = from_float<T>(fit<T>(v[k], sat));
+                *y = from_float<T>(fit<T>(v[k], largest));
               }
             }
           }
         }
       }
-      if (sat) record_error(p.err, MOE_ERR_RANGE);
+      if (largest > 65504.f) record_error(p.err, MOE_ERR_RANGE);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
