@@ -1,0 +1,38 @@
+// launch.cuh -- launches that overlap the kernel before them in the stream: the
+// grid may be set up, and its blocks may run up to previous_done(), while the
+// last blocks of that kernel finish.  A kernel launched this way calls
+// previous_done() before it touches any memory that another one may write or
+// read; it returns when all kernels before it have completed and their writes
+// can be seen.  (Back to back, 64 x 6144 x 12288 in 8 bits: 22.3 -> 21.3 us a
+// product; one row of 6144 to 8 bits: 2.8 -> 2.55 us, and back 1.67 -> 1.3.)
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <utility>
+
+namespace srm {
+
+// Every block of a grid says that the next kernel may be set up (it has all its
+// resources by then) before it waits for the previous one.
+__device__ __forceinline__ void previous_done() {
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,
+                              cudaStream_t stream, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+}  // namespace srm

@@ -31,6 +31,7 @@
 #include <cuda.h>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "rowio.cuh"
 
 namespace srm {
@@ -268,7 +269,6 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
     }
     mbar_init(&s.drain, 1);
     s.abort_flag = 0;
-    s.ready = *p.ready == kQ8Ready;
     s.mma_consumed = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmap_tok);
@@ -284,6 +284,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       tmem_relinquish();
     }
   }
+  previous_done();
+  if (threadIdx.x == 64) s.ready = *p.ready == kQ8Ready;
   if (warp == 0) {
     // Group offsets and an exclusive scan of ceil(rows / BT).  The offsets are
     // the caller's: a group whose range is not 0 <= o0 <= o1 <= R, or a first
@@ -784,15 +786,15 @@ cudaError_t launch_t(const TokMaps &tok, const CUtensorMap &tw, const Q8GemmArgs
     constexpr size_t smem = smem_bytes<true>();
     e = prepare_kernel(kern, smem, true, num_sms, &resident);
     if (e != cudaSuccess) return e;
-    kern<<<2 * static_cast<unsigned>(p.units < resident ? p.units : resident), THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
-  } else {
-    auto kern = q8_gemm_solo_kernel<kSwiglu, T>;
-    constexpr size_t smem = smem_bytes<false>();
-    e = prepare_kernel(kern, smem, false, num_sms, &resident);
-    if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(p.units < resident ? p.units : resident), THREADS, smem, stream>>>(tok.small, tok.big, tw, p);
+    return launch_overlapped(kern, 2 * static_cast<unsigned>(p.units < resident ? p.units : resident), THREADS, smem,
+                             stream, tok.small, tok.big, tw, p);
   }
-  return cudaGetLastError();
+  auto kern = q8_gemm_solo_kernel<kSwiglu, T>;
+  constexpr size_t smem = smem_bytes<false>();
+  e = prepare_kernel(kern, smem, false, num_sms, &resident);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(kern, static_cast<unsigned>(p.units < resident ? p.units : resident), THREADS, smem,
+                           stream, tok.small, tok.big, tw, p);
 }
 }  // namespace q8
 

@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "rowio.cuh"
 
 namespace srm {
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
   const int tpr = kWarps == 1 ? 32 : blockDim.x;
   const int64_t t = kWarps == 1 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : blockIdx.x;
   if (t >= p.T) return;  // whole warps (or CTAs) only
+  previous_done();
   const T *x = static_cast<const T *>(p.x) + t * p.ld_x;
   const T *delta = p.delta ? static_cast<const T *>(p.delta) + t * p.ld_delta : nullptr;
   const T *gamma = static_cast<const T *>(p.gamma);
@@ -234,6 +236,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
   const int tpr = kWarps == 1 ? 32 : blockDim.x;
   const int64_t t = kWarps == 1 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : blockIdx.x;
   if (t >= p.T) return;  // whole warps (or CTAs) only
+  previous_done();
   const T *x = static_cast<const T *>(p.x) + t * p.ld_x;
   typename Io::Raw rx[U];
   const int last = p.H - E;
@@ -269,6 +272,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024) q8_long_rows_kernel(const Q8RowArgs p) {
   __shared__ float sum_buf[2][32];
   __shared__ uint32_t max_buf[32];
+  previous_done();
   const int64_t t = blockIdx.x;
   const T *x = static_cast<const T *>(p.x) + t * p.ld_x;
   const T *delta = p.delta ? static_cast<const T *>(p.delta) + t * p.ld_delta : nullptr;
@@ -316,6 +320,7 @@ __global__ void __launch_bounds__(256)
   const int tid = threadIdx.x & (tpr - 1);
   const int64_t t = (static_cast<int64_t>(blockIdx.x) << (8 - tpr_log2)) + (threadIdx.x >> tpr_log2);
   if (t >= T_) return;
+  previous_done();
   const int8_t *src = q + t * ld_q;
   T *dst = y + t * ld_y;
   const float s = scale[t];
@@ -359,11 +364,8 @@ cudaError_t launch_rows_u(const Q8RowArgs &p, cudaStream_t stream) {
   const bool plain = !p.delta && !p.gamma && !p.x_sum && !p.y;
   auto go = [&](auto full, auto quantize) {
     auto kern = plain ? quantize : full;
-    if (threads <= 32)
-      kern<<<(rows + 3) / 4, 128, 0, stream>>>(p);
-    else
-      kern<<<rows, threads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return threads <= 32 ? launch_overlapped(kern, (rows + 3) / 4, 128, 0, stream, p)
+                         : launch_overlapped(kern, rows, threads, 0, stream, p);
   };
   if (threads <= 32) return go(q8_rows_kernel<T, E, U, 1>, q8_quantize_kernel<T, E, U, 1>);
   if (threads <= 256) return go(q8_rows_kernel<T, E, U, 8>, q8_quantize_kernel<T, E, U, 8>);
@@ -377,8 +379,7 @@ cudaError_t launch_rows_e(const Q8RowArgs &p, int num_sms, cudaStream_t stream) 
   const int loads = (p.H + E - 1) / E;
   if (loads <= 1024 && p.T <= 2 * num_sms) return launch_rows_u<T, E, 1>(p, stream);
   if (loads <= U * (E == 1 ? 512 : 1024)) return launch_rows_u<T, E, U>(p, stream);
-  q8_long_rows_kernel<T><<<static_cast<unsigned>(p.T), 1024, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(q8_long_rows_kernel<T>, static_cast<unsigned>(p.T), 1024, 0, stream, p);
 }
 
 template <typename T>
@@ -405,11 +406,8 @@ cudaError_t launch_dequant_t(const int8_t *q, const float *scale, void *y, int64
   int log2 = 0;  // threads per row: four loads each
   while (log2 < 8 && (4 << log2) < loads) ++log2;
   const unsigned blocks = static_cast<unsigned>((T_ + (256 >> log2) - 1) >> (8 - log2));
-  if (vec)
-    q8_dequantize_kernel<T, E><<<blocks, 256, 0, stream>>>(q, scale, static_cast<T *>(y), T_, H, ld_q, ld_y, log2);
-  else
-    q8_dequantize_kernel<T, 1><<<blocks, 256, 0, stream>>>(q, scale, static_cast<T *>(y), T_, H, ld_q, ld_y, log2);
-  return cudaGetLastError();
+  return launch_overlapped(vec ? q8_dequantize_kernel<T, E> : q8_dequantize_kernel<T, 1>, blocks, 256, 0, stream, q,
+                           scale, static_cast<T *>(y), T_, H, ld_q, ld_y, log2);
 }
 
 }  // namespace

@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "rowio.cuh"
 
 namespace srm {
@@ -81,6 +82,7 @@ constexpr int kSmallPositions = 4096;  // the inverse in every CTA's shared memo
 __global__ void __launch_bounds__(256)
     rows_invert_kernel(const RowsArgs p, const int32_t *__restrict__ offsets,
                        const int32_t *__restrict__ sorted, int32_t *__restrict__ pos) {
+  previous_done();
   const int n = row_total(offsets, p.E + 1, p.P, p.err);
   for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
     const int a = sorted[i];
@@ -150,6 +152,7 @@ __global__ void __launch_bounds__(256)
                         uint8_t *__restrict__ xs, const float *__restrict__ x_scale,
                         float *__restrict__ xs_scale, int64_t row_bytes, int64_t x_pitch, int64_t xs_pitch,
                         int wpt) {
+  previous_done();
   scatter_tokens<W>(p, pos, x, xs, x_scale, xs_scale, row_bytes, x_pitch, xs_pitch, wpt);
 }
 
@@ -166,6 +169,7 @@ __global__ void __launch_bounds__(256)
   __shared__ int32_t inverse[kSmallPositions];
   for (int i = threadIdx.x; i < p.P; i += 256) inverse[i] = -1;
   __syncthreads();
+  previous_done();
   const int n = row_total(offsets, p.E + 1, p.P, p.err);
   for (int i = threadIdx.x; i < n; i += 256) {
     const int a = sorted[i];
@@ -192,6 +196,7 @@ __global__ void __launch_bounds__(256)
   const int tpr = 1 << tpr_log2;
   const int64_t t64 = (static_cast<int64_t>(blockIdx.x) << (8 - tpr_log2)) + (threadIdx.x >> tpr_log2);
   if (t64 >= p.T) return;
+  previous_done();
   const int t = static_cast<int>(t64);
   const int n = kExact ? NB : p.K + p.has_shared;
   int at[NB];
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__(256)
                             float *dgate, int wpt) {
   constexpr int B = 4;
   __shared__ float partial[8][16];
+  previous_done();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t64 = static_cast<int64_t>(blockIdx.x) * (8 / wpt) + warp / wpt;
   const int t = static_cast<int>(t64);
@@ -367,20 +373,17 @@ cudaError_t launch_sort_w(const RowsArgs &p, const SortPtrs &a, int elem, int nu
   uint8_t *xs = static_cast<uint8_t *>(a.xs);
   const int64_t row = static_cast<int64_t>(p.H) * elem;
   if (p.P <= kSmallPositions) {
-    rows_sort_small_kernel<W><<<grid, 256, 0, stream>>>(p, a.offsets, a.sorted, a.pos, x, xs, a.x_scale,
-                                                        a.xs_scale, row, p.ld_token * elem, p.ld_slot * elem, wpt);
-    return cudaGetLastError();
+    return launch_overlapped(rows_sort_small_kernel<W>, grid, 256, 0, stream, p, a.offsets, a.sorted, a.pos, x, xs,
+                             a.x_scale, a.xs_scale, row, p.ld_token * elem, p.ld_slot * elem, wpt);
   }
   cudaError_t e = cudaMemsetAsync(a.pos, 0xff, sizeof(int32_t) * static_cast<size_t>(p.P), stream);
   if (e != cudaSuccess) return e;
   const int64_t inv = (p.P + 255ll) / 256, inv_cap = num_sms * 8ll;
-  rows_invert_kernel<<<static_cast<unsigned>(inv < inv_cap ? inv : inv_cap), 256, 0, stream>>>(p, a.offsets,
-                                                                                              a.sorted, a.pos);
-  e = cudaGetLastError();
+  e = launch_overlapped(rows_invert_kernel, static_cast<unsigned>(inv < inv_cap ? inv : inv_cap), 256, 0, stream, p,
+                        a.offsets, a.sorted, a.pos);
   if (e != cudaSuccess) return e;
-  rows_scatter_kernel<W><<<grid, 256, 0, stream>>>(p, a.pos, x, xs, a.x_scale, a.xs_scale, row,
-                                                   p.ld_token * elem, p.ld_slot * elem, wpt);
-  return cudaGetLastError();
+  return launch_overlapped(rows_scatter_kernel<W>, grid, 256, 0, stream, p, a.pos, x, xs, a.x_scale, a.xs_scale,
+                           row, p.ld_token * elem, p.ld_slot * elem, wpt);
 }
 
 template <typename Tt, typename Ts, int E>
@@ -391,23 +394,16 @@ cudaError_t launch_unsort_e(const RowsArgs &p, const void *ys, const float *gate
   while (log2 < 8 && (1 << log2) < units) ++log2;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.T) + (256 >> log2) - 1) >> (8 - log2));
   auto go = [&](auto kern) {
-    kern<<<grid, 256, 0, stream>>>(p, static_cast<const Ts *>(ys), gate, pos,
-                                   static_cast<const Tt *>(residual), static_cast<Tt *>(y), log2);
+    return launch_overlapped(kern, grid, 256, 0, stream, p, static_cast<const Ts *>(ys), gate, pos,
+                             static_cast<const Tt *>(residual), static_cast<Tt *>(y), log2);
   };
   const int n = p.K + p.has_shared;
-  if (n == 4)
-    go(rows_unsort_kernel<Tt, Ts, E, 4, true>);
-  else if (n == 5)
-    go(rows_unsort_kernel<Tt, Ts, E, 5, true>);
-  else if (n == 8)
-    go(rows_unsort_kernel<Tt, Ts, E, 8, true>);
-  else if (n == 9)
-    go(rows_unsort_kernel<Tt, Ts, E, 9, true>);
-  else if (n < 8)
-    go(rows_unsort_kernel<Tt, Ts, E, 7, false>);
-  else
-    go(rows_unsort_kernel<Tt, Ts, E, 17, false>);
-  return cudaGetLastError();
+  if (n == 4) return go(rows_unsort_kernel<Tt, Ts, E, 4, true>);
+  if (n == 5) return go(rows_unsort_kernel<Tt, Ts, E, 5, true>);
+  if (n == 8) return go(rows_unsort_kernel<Tt, Ts, E, 8, true>);
+  if (n == 9) return go(rows_unsort_kernel<Tt, Ts, E, 9, true>);
+  if (n < 8) return go(rows_unsort_kernel<Tt, Ts, E, 7, false>);
+  return go(rows_unsort_kernel<Tt, Ts, E, 17, false>);
 }
 
 template <typename Tt, typename Ts, int E>
@@ -416,9 +412,8 @@ cudaError_t launch_grad_e(const RowsArgs &p, const void *dy, const void *ys, con
   int wpt = 1;
   while (wpt < 8 && static_cast<int64_t>(p.T) * wpt < num_sms * 32) wpt *= 2;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.T) + 8 / wpt - 1) / (8 / wpt));
-  rows_unsort_grad_kernel<Tt, Ts, E><<<grid, 256, 0, stream>>>(
-      p, static_cast<const Tt *>(dy), static_cast<const Ts *>(ys), gate, pos, static_cast<Ts *>(dys), dgate, wpt);
-  return cudaGetLastError();
+  return launch_overlapped(rows_unsort_grad_kernel<Tt, Ts, E>, grid, 256, 0, stream, p, static_cast<const Tt *>(dy),
+                           static_cast<const Ts *>(ys), gate, pos, static_cast<Ts *>(dys), dgate, wpt);
 }
 
 // f(Tt{}, Ts{}) for the two element types

@@ -19,7 +19,7 @@ def elsewhere(t, stream) -> bool:
         raise TypeError("expected a torch.Tensor, got %s" % type(t).__name__)
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device, got %s" % t.device)
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+    return stream is not None or t.get_device() != _current_device()
 
 
 def on(t, stream):
@@ -32,24 +32,19 @@ def on(t, stream):
     return torch.cuda.stream(stream)
 
 
-def raw_stream(t) -> int:
-    """The current stream of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+# the current stream of a device, as an address
+raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice  # CUDA is up: there is a CUDA tensor
 
 
-def mat(t, name, shape, dtype, like):
-    """(address, row stride) of a matrix `shape` of `dtype` with contiguous rows, on `like`'s device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.is_cuda and t.get_device() == like.get_device()):
-        return t.data_ptr(), shape[1]
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != like.device:
-        raise ValueError("%s is on %s, the call on %s" % (name, t.device, like.device))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+def mat(t, name, shape, dtype, device):
+    """(address, row stride) of a matrix `shape` of `dtype` with contiguous rows on CUDA device `device`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr(), shape[1]
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % name) from None
+    _check(t, name, shape, dtype, device)
     if shape[1] > 1 and t.stride(1) != 1 and shape[0] > 0:
         raise ValueError("%s must have contiguous rows" % name)
     if shape[0] > 1 and t.stride(0) < shape[1]:
@@ -57,20 +52,24 @@ def mat(t, name, shape, dtype, like):
     return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
 
 
-def vec(t, name, shape, dtype, like) -> int:
-    """The address of a contiguous tensor `shape` of `dtype` on `like`'s device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.is_cuda and t.get_device() == like.get_device()):
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != like.device:
-        raise ValueError("%s is on %s, the call on %s" % (name, t.device, like.device))
+def vec(t, name, shape, dtype, device) -> int:
+    """The address of a contiguous tensor `shape` of `dtype` on CUDA device `device`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % name) from None
+    _check(t, name, shape, dtype, device)
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _check(t, name, shape, dtype, device):
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, the call on cuda:%d" % (name, t.device, device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    raise ValueError("%s must be contiguous" % name)
 
 
 def rows_of(t, name, dtypes):
@@ -82,10 +81,10 @@ def rows_of(t, name, dtypes):
     return t.shape
 
 
-def workspace(ws, least, like) -> int:
+def workspace(ws, least, device) -> int:
     """The address of a uint8 workspace of at least `least` bytes."""
     if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.numel() < least:
         raise TypeError("ws must be a uint8 tensor of at least %d bytes" % least)
-    if ws.device != like.device:
-        raise ValueError("ws is on %s, the call on %s" % (ws.device, like.device))
+    if ws.get_device() != device:
+        raise ValueError("ws is on %s, the call on cuda:%d" % (ws.device, device))
     return ws.data_ptr()

@@ -42,14 +42,14 @@ class _Matmul(ctypes.Structure):
                 ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_residual", ctypes.c_int64)]
 
 
-_bound = False
+_lib = None
 
 
 def lib():
     """The library with the 8-bit entry points typed."""
-    global _bound
-    L = moe.lib()
-    if not _bound:
+    global _lib
+    if _lib is None:
+        L = moe.lib()
         vp, P = ctypes.c_void_p, ctypes.POINTER
         L.moe_q8_add_rmsnorm.restype = ctypes.c_int
         L.moe_q8_add_rmsnorm.argtypes = [P(_Rows), vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp]
@@ -65,20 +65,19 @@ def lib():
         L.moe_q8_workspace_init.argtypes = [vp, ctypes.c_size_t, vp]
         L.moe_q8_matmul.restype = ctypes.c_int
         L.moe_q8_matmul.argtypes = [P(_Matmul)] + [vp] * 8 + [ctypes.c_size_t, vp]
-        _bound = True
-    return L
+        _lib = L
+    return _lib
 
 
 # ------------------------------------------------------------------ rows in 8 bits
 
-def _q_out(out, x, shape):
+def _q_out(out, x, shape, dev):
     if out is None:
-        q, scale = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format), x.new_empty(
-            (shape[0],), dtype=torch.float32)
+        q, scale = x.new_empty(shape, dtype=torch.int8), x.new_empty(shape[0], dtype=torch.float32)
         return q, q.data_ptr(), shape[1], scale, scale.data_ptr()
     q, scale = out
-    q_ptr, ld_q = mat(q, "q", shape, torch.int8, x)
-    return q, q_ptr, ld_q, scale, vec(scale, "scale", (shape[0],), torch.float32, x)
+    q_ptr, ld_q = mat(q, "q", shape, torch.int8, dev)
+    return q, q_ptr, ld_q, scale, vec(scale, "scale", shape[:1], torch.float32, dev)
 
 
 def add_rmsnorm(x, gamma, eps=1e-5, delta=None, x_out=None, y=None, out=None, stream=None):
@@ -89,15 +88,15 @@ def add_rmsnorm(x, gamma, eps=1e-5, delta=None, x_out=None, y=None, out=None, st
     if elsewhere(x, stream):
         with on(x, stream):
             return add_rmsnorm(x, gamma, eps, delta, x_out, y, out)
-    shape, t = rows_of(x, "x", FLOATS), x.dtype
-    x_ptr, ld = mat(x, "x", shape, t, x)
-    g_ptr = vec(gamma, "gamma", shape[1:], t, x)
-    d_ptr, ld_d = mat(delta, "delta", shape, t, x) if delta is not None else (None, 0)
-    s_ptr, ld_s = mat(x_out, "x_out", shape, t, x) if x_out is not None else (None, 0)
-    y_ptr, ld_y = mat(y, "y", shape, t, x) if y is not None else (None, 0)
-    q, q_ptr, ld_q, scale, scale_ptr = _q_out(out, x, shape)
+    shape, t, dev = rows_of(x, "x", FLOATS), x.dtype, x.get_device()
+    x_ptr, ld = mat(x, "x", shape, t, dev)
+    g_ptr = vec(gamma, "gamma", shape[1:], t, dev)
+    d_ptr, ld_d = mat(delta, "delta", shape, t, dev) if delta is not None else (None, 0)
+    s_ptr, ld_s = mat(x_out, "x_out", shape, t, dev) if x_out is not None else (None, 0)
+    y_ptr, ld_y = mat(y, "y", shape, t, dev) if y is not None else (None, 0)
+    q, q_ptr, ld_q, scale, scale_ptr = _q_out(out, x, shape, dev)
     c = _Rows(shape[0], shape[1], DTYPES[t], ld, ld_d, ld_s, ld_y, ld_q)
-    rc = lib().moe_q8_add_rmsnorm(c, x_ptr, d_ptr, g_ptr, eps, s_ptr, y_ptr, q_ptr, scale_ptr, raw_stream(x))
+    rc = (_lib or lib()).moe_q8_add_rmsnorm(c, x_ptr, d_ptr, g_ptr, eps, s_ptr, y_ptr, q_ptr, scale_ptr, raw_stream(dev))
     if rc:
         raise moe.MoeError(rc, "moe_q8_add_rmsnorm")
     return q, scale
@@ -108,11 +107,11 @@ def quantize(x, out=None, stream=None):
     if elsewhere(x, stream):
         with on(x, stream):
             return quantize(x, out)
-    shape, t = rows_of(x, "x", FLOATS), x.dtype
-    x_ptr, ld = mat(x, "x", shape, t, x)
-    q, q_ptr, ld_q, scale, scale_ptr = _q_out(out, x, shape)
-    rc = lib().moe_q8_quantize(_Rows(shape[0], shape[1], DTYPES[t], ld, 0, 0, 0, ld_q), x_ptr, q_ptr, scale_ptr,
-                               raw_stream(x))
+    shape, t, dev = rows_of(x, "x", FLOATS), x.dtype, x.get_device()
+    x_ptr, ld = mat(x, "x", shape, t, dev)
+    q, q_ptr, ld_q, scale, scale_ptr = _q_out(out, x, shape, dev)
+    rc = (_lib or lib()).moe_q8_quantize(_Rows(shape[0], shape[1], DTYPES[t], ld, 0, 0, 0, ld_q), x_ptr, q_ptr,
+                                         scale_ptr, raw_stream(dev))
     if rc:
         raise moe.MoeError(rc, "moe_q8_quantize")
     return q, scale
@@ -123,16 +122,18 @@ def dequantize(q, scale, dtype=torch.bfloat16, out=None, stream=None):
     if elsewhere(q, stream):
         with on(q, stream):
             return dequantize(q, scale, dtype, out)
-    shape = rows_of(q, "q", (torch.int8,))
+    shape, dev = rows_of(q, "q", (torch.int8,)), q.get_device()
     if dtype not in FLOATS:
         raise TypeError("dtype must be %s, got %s" % (" or ".join(map(str, FLOATS)), dtype))
-    q_ptr, ld_q = mat(q, "q", shape, torch.int8, q)
-    scale_ptr = vec(scale, "scale", shape[:1], torch.float32, q)
+    q_ptr, ld_q = mat(q, "q", shape, torch.int8, dev)
+    scale_ptr = vec(scale, "scale", shape[:1], torch.float32, dev)
     if out is None:
         out = q.new_empty(shape, dtype=dtype)
-    y_ptr, ld_y = mat(out, "out", shape, dtype, q)
-    rc = lib().moe_q8_dequantize(_Rows(shape[0], shape[1], DTYPES[dtype], 0, 0, 0, ld_y, ld_q), q_ptr, scale_ptr,
-                                 y_ptr, raw_stream(q))
+        y_ptr, ld_y = out.data_ptr(), shape[1]
+    else:
+        y_ptr, ld_y = mat(out, "out", shape, dtype, dev)
+    rc = (_lib or lib()).moe_q8_dequantize(_Rows(shape[0], shape[1], DTYPES[dtype], 0, 0, 0, ld_y, ld_q), q_ptr,
+                                           scale_ptr, y_ptr, raw_stream(dev))
     if rc:
         raise moe.MoeError(rc, "moe_q8_dequantize")
     return out
@@ -161,7 +162,7 @@ def pack_weights(cfg: moe.Config, w1, w3, w2, ws1=None, ws3=None, ws2=None, stre
         moe._check(lib().moe_q8_pack_weights(ctypes.byref(cfg.c()), moe._ptr(w1), moe._ptr(w3), moe._ptr(w2),
                                              moe._ptr(ws1), moe._ptr(ws3), moe._ptr(ws2), moe._ptr(w13),
                                              moe._ptr(w13_scale), moe._ptr(w2q), moe._ptr(w2_scale),
-                                             raw_stream(like)), "moe_q8_pack_weights")
+                                             raw_stream(like.get_device())), "moe_q8_pack_weights")
     return w13, w13_scale, w2q, w2_scale
 
 
@@ -205,7 +206,8 @@ def init_workspace(ws):
     """Sets a workspace's control words: once for memory allocated elsewhere, and after a call that
     reported MOE_ERR_TIMEOUT."""
     with on(ws, None):
-        moe._check(lib().moe_q8_workspace_init(workspace_ptr(ws, 256, ws), ws.numel(), raw_stream(ws)),
+        dev = ws.get_device()
+        moe._check(lib().moe_q8_workspace_init(workspace_ptr(ws, 256, dev), ws.numel(), raw_stream(dev)),
                    "moe_q8_workspace_init")
 
 
@@ -216,24 +218,27 @@ def matmul(cfg: MatmulConfig, x, x_scale, w, w_scale, ws, offsets=None, residual
     if elsewhere(x, stream):
         with on(x, stream):
             return matmul(cfg, x, x_scale, w, w_scale, ws, offsets, residual, out)
-    R, N, K, G, t = cfg.R, cfg.N, cfg.K, cfg.groups, cfg.dtype
+    R, N, K, G, t, dev = cfg.R, cfg.N, cfg.K, cfg.groups, cfg.dtype, x.get_device()
     shape = (R, N // 2 if cfg.swiglu else N)
-    x_ptr, ld_x = mat(x, "x", (R, K), torch.int8, x)
-    xs_ptr = vec(x_scale, "x_scale", (R,), torch.float32, x)
-    w_ptr = vec(w, "w", (G * N, K), torch.int8, x)
-    ws_ptr = vec(w_scale, "w_scale", (G * N,), torch.float32, x)
+    x_ptr, ld_x = mat(x, "x", (R, K), torch.int8, dev)
+    xs_ptr = vec(x_scale, "x_scale", (R,), torch.float32, dev)
+    w_ptr = vec(w, "w", (G * N, K), torch.int8, dev)
+    ws_ptr = vec(w_scale, "w_scale", (G * N,), torch.float32, dev)
     off_ptr = None
     if offsets is not None:
         if offsets.dim() != 1 or offsets.shape[0] < G + 1:
             raise ValueError("offsets must have at least %d entries" % (G + 1))
-        off_ptr = vec(offsets, "offsets", offsets.shape, torch.int32, x)
-    r_ptr, ld_r = mat(residual, "residual", shape, t, x) if residual is not None else (None, 0)
-    work = workspace_ptr(ws, 256, x)
+        off_ptr = vec(offsets, "offsets", offsets.shape, torch.int32, dev)
+    r_ptr, ld_r = mat(residual, "residual", shape, t, dev) if residual is not None else (None, 0)
+    work = workspace_ptr(ws, 256, dev)
     if out is None:
         out = x.new_empty(shape, dtype=t)
-    y_ptr, ld_y = mat(out, "out", shape, t, x)
+        y_ptr, ld_y = out.data_ptr(), shape[1]
+    else:
+        y_ptr, ld_y = mat(out, "out", shape, t, dev)
     c = _Matmul(R, N, K, G, 1 if cfg.swiglu else 0, DTYPES.get(t, -1), ld_x, ld_y, ld_r)
-    rc = lib().moe_q8_matmul(c, x_ptr, xs_ptr, w_ptr, ws_ptr, off_ptr, r_ptr, y_ptr, work, ws.numel(), raw_stream(x))
+    rc = (_lib or lib()).moe_q8_matmul(c, x_ptr, xs_ptr, w_ptr, ws_ptr, off_ptr, r_ptr, y_ptr, work, ws.numel(),
+                                       raw_stream(dev))
     if rc:
         raise moe.MoeError(rc, "moe_q8_matmul")
     return out

@@ -65,22 +65,22 @@ class Config:
                     DTYPES.get(self.slot_dtype, -1), ld_token, ld_slot, ld_residual, ld_dys)
 
 
-_bound = False
+_lib = None
 
 
 def lib():
     """The library with the row entry points typed."""
-    global _bound
-    L = moe.lib()
-    if not _bound:
+    global _lib
+    if _lib is None:
+        L = moe.lib()
         vp, P = ctypes.c_void_p, ctypes.POINTER
         for name, n in (("moe_rows_sort", 9), ("moe_rows_unsort", 7), ("moe_rows_sort_grad", 5),
                         ("moe_rows_unsort_grad", 8)):
             f = getattr(L, name)
             f.restype = ctypes.c_int
             f.argtypes = [P(_Cfg)] + [vp] * n
-        _bound = True
-    return L
+        _lib = L
+    return _lib
 
 
 def workspace(device=None) -> torch.Tensor:
@@ -88,9 +88,23 @@ def workspace(device=None) -> torch.Tensor:
     return torch.zeros(256, dtype=torch.uint8, device=device or "cuda")
 
 
-def _pos_gate(cfg, pos, gate, like):
-    pos_ptr = vec(pos, "pos", (cfg.rows,), torch.int32, like)
-    return pos_ptr, vec(gate, "gate", (cfg.T, cfg.K), torch.float32, like) if gate is not None else None
+def _pos_gate(cfg, pos, gate, dev):
+    pos_ptr = vec(pos, "pos", (cfg.rows,), torch.int32, dev)
+    return pos_ptr, vec(gate, "gate", (cfg.T, cfg.K), torch.float32, dev) if gate is not None else None
+
+
+def _mat_out(out, like, name, shape, dtype, dev):
+    if out is None:
+        out = like.new_empty(shape, dtype=dtype)
+        return out, out.data_ptr(), shape[1]
+    return out, *mat(out, name, shape, dtype, dev)
+
+
+def _vec_out(out, like, name, shape, dtype, dev):
+    if out is None:
+        out = like.new_empty(shape, dtype=dtype)
+        return out, out.data_ptr()
+    return out, vec(out, name, shape, dtype, dev)
 
 
 def sort(cfg: Config, x, offsets, sorted_, ws, x_scale=None, out=None, pos=None, xs_scale=None, stream=None):
@@ -99,26 +113,21 @@ def sort(cfg: Config, x, offsets, sorted_, ws, x_scale=None, out=None, pos=None,
     if elsewhere(x, stream):
         with on(x, stream):
             return sort(cfg, x, offsets, sorted_, ws, x_scale, out, pos, xs_scale)
-    P, H, t = cfg.rows, cfg.H, cfg.dtype
-    x_ptr, ld = mat(x, "x", (cfg.T, H), t, x)
-    off_ptr = vec(offsets, "offsets", (cfg.E + 2,), torch.int32, x)
-    ids_ptr = vec(sorted_, "sorted", (P,), torch.int32, x)
-    ws_ptr = workspace_ptr(ws, 256, x)
-    xs = x.new_empty((P, H)) if out is None else out
-    xs_ptr, ld_s = mat(xs, "out", (P, H), t, x)
-    if pos is None:
-        pos = x.new_empty((P,), dtype=torch.int32)
-    pos_ptr = vec(pos, "pos", (P,), torch.int32, x)
+    P, H, t, dev = cfg.rows, cfg.H, cfg.dtype, x.get_device()
+    x_ptr, ld = mat(x, "x", (cfg.T, H), t, dev)
+    off_ptr = vec(offsets, "offsets", (cfg.E + 2,), torch.int32, dev)
+    ids_ptr = vec(sorted_, "sorted", (P,), torch.int32, dev)
+    ws_ptr = workspace_ptr(ws, 256, dev)
+    xs, xs_ptr, ld_s = _mat_out(out, x, "out", (P, H), t, dev)
+    pos, pos_ptr = _vec_out(pos, x, "pos", (P,), torch.int32, dev)
     scale_ptr = xs_scale_ptr = None
     if x_scale is not None:
-        scale_ptr = vec(x_scale, "x_scale", (cfg.T,), torch.float32, x)
-        if xs_scale is None:
-            xs_scale = x.new_empty((P,), dtype=torch.float32)
-        xs_scale_ptr = vec(xs_scale, "xs_scale", (P,), torch.float32, x)
+        scale_ptr = vec(x_scale, "x_scale", (cfg.T,), torch.float32, dev)
+        xs_scale, xs_scale_ptr = _vec_out(xs_scale, x, "xs_scale", (P,), torch.float32, dev)
     elif xs_scale is not None:
         raise ValueError("xs_scale without x_scale")
-    rc = lib().moe_rows_sort(cfg.c(ld, ld_s), x_ptr, scale_ptr, off_ptr, ids_ptr, pos_ptr, xs_ptr, xs_scale_ptr,
-                             ws_ptr, raw_stream(x))
+    rc = (_lib or lib()).moe_rows_sort(cfg.c(ld, ld_s), x_ptr, scale_ptr, off_ptr, ids_ptr, pos_ptr, xs_ptr,
+                                       xs_scale_ptr, ws_ptr, raw_stream(dev))
     if rc:
         raise moe.MoeError(rc, "moe_rows_sort")
     return (xs, pos) if x_scale is None else (xs, xs_scale, pos)
@@ -130,14 +139,14 @@ def unsort(cfg: Config, ys, gate, pos, ws, residual=None, out=None, stream=None)
     if elsewhere(ys, stream):
         with on(ys, stream):
             return unsort(cfg, ys, gate, pos, ws, residual, out)
-    shape, t = (cfg.T, cfg.H), cfg.dtype
-    ys_ptr, ld_s = mat(ys, "ys", (cfg.rows, cfg.H), cfg.slot_dtype, ys)
-    pos_ptr, gate_ptr = _pos_gate(cfg, pos, gate, ys)
-    r_ptr, ld_r = mat(residual, "residual", shape, t, ys) if residual is not None else (None, 0)
-    ws_ptr = workspace_ptr(ws, 256, ys)
-    y = ys.new_empty(shape, dtype=t) if out is None else out
-    y_ptr, ld = mat(y, "out", shape, t, ys)
-    rc = lib().moe_rows_unsort(cfg.c(ld, ld_s, ld_r), ys_ptr, gate_ptr, pos_ptr, r_ptr, y_ptr, ws_ptr, raw_stream(ys))
+    shape, t, dev = (cfg.T, cfg.H), cfg.dtype, ys.get_device()
+    ys_ptr, ld_s = mat(ys, "ys", (cfg.rows, cfg.H), cfg.slot_dtype, dev)
+    pos_ptr, gate_ptr = _pos_gate(cfg, pos, gate, dev)
+    r_ptr, ld_r = mat(residual, "residual", shape, t, dev) if residual is not None else (None, 0)
+    ws_ptr = workspace_ptr(ws, 256, dev)
+    y, y_ptr, ld = _mat_out(out, ys, "out", shape, t, dev)
+    rc = (_lib or lib()).moe_rows_unsort(cfg.c(ld, ld_s, ld_r), ys_ptr, gate_ptr, pos_ptr, r_ptr, y_ptr, ws_ptr,
+                                         raw_stream(dev))
     if rc:
         raise moe.MoeError(rc, "moe_rows_unsort")
     return y
@@ -148,12 +157,12 @@ def sort_grad(cfg: Config, dxs, pos, ws, out=None, stream=None):
     if elsewhere(dxs, stream):
         with on(dxs, stream):
             return sort_grad(cfg, dxs, pos, ws, out)
-    dxs_ptr, ld_s = mat(dxs, "dxs", (cfg.rows, cfg.H), cfg.dtype, dxs)
-    pos_ptr, _ = _pos_gate(cfg, pos, None, dxs)
-    ws_ptr = workspace_ptr(ws, 256, dxs)
-    dx = dxs.new_empty((cfg.T, cfg.H)) if out is None else out
-    dx_ptr, ld = mat(dx, "out", (cfg.T, cfg.H), cfg.dtype, dxs)
-    rc = lib().moe_rows_sort_grad(cfg.c(ld, ld_s), dxs_ptr, pos_ptr, dx_ptr, ws_ptr, raw_stream(dxs))
+    t, dev = cfg.dtype, dxs.get_device()
+    dxs_ptr, ld_s = mat(dxs, "dxs", (cfg.rows, cfg.H), t, dev)
+    pos_ptr, _ = _pos_gate(cfg, pos, None, dev)
+    ws_ptr = workspace_ptr(ws, 256, dev)
+    dx, dx_ptr, ld = _mat_out(out, dxs, "out", (cfg.T, cfg.H), t, dev)
+    rc = (_lib or lib()).moe_rows_sort_grad(cfg.c(ld, ld_s), dxs_ptr, pos_ptr, dx_ptr, ws_ptr, raw_stream(dev))
     if rc:
         raise moe.MoeError(rc, "moe_rows_sort_grad")
     return dx
@@ -165,18 +174,15 @@ def unsort_grad(cfg: Config, dy, ys, gate, pos, ws, out=None, dgate=None, stream
     if elsewhere(dy, stream):
         with on(dy, stream):
             return unsort_grad(cfg, dy, ys, gate, pos, ws, out, dgate)
-    slots, t = (cfg.rows, cfg.H), cfg.slot_dtype
-    dy_ptr, ld = mat(dy, "dy", (cfg.T, cfg.H), cfg.dtype, dy)
-    ys_ptr, ld_s = mat(ys, "ys", slots, t, dy)
-    pos_ptr, gate_ptr = _pos_gate(cfg, pos, gate, dy)
-    ws_ptr = workspace_ptr(ws, 256, dy)
-    dys = dy.new_empty(slots, dtype=t) if out is None else out
-    dys_ptr, ld_d = mat(dys, "out", slots, t, dy)
-    if dgate is None:
-        dgate = dy.new_empty((cfg.T, cfg.K), dtype=torch.float32)
-    dgate_ptr = vec(dgate, "dgate", (cfg.T, cfg.K), torch.float32, dy)
-    rc = lib().moe_rows_unsort_grad(cfg.c(ld, ld_s, 0, ld_d), dy_ptr, ys_ptr, gate_ptr, pos_ptr, dys_ptr, dgate_ptr,
-                                    ws_ptr, raw_stream(dy))
+    slots, t, dev = (cfg.rows, cfg.H), cfg.slot_dtype, dy.get_device()
+    dy_ptr, ld = mat(dy, "dy", (cfg.T, cfg.H), cfg.dtype, dev)
+    ys_ptr, ld_s = mat(ys, "ys", slots, t, dev)
+    pos_ptr, gate_ptr = _pos_gate(cfg, pos, gate, dev)
+    ws_ptr = workspace_ptr(ws, 256, dev)
+    dys, dys_ptr, ld_d = _mat_out(out, dy, "out", slots, t, dev)
+    dgate, dgate_ptr = _vec_out(dgate, dy, "dgate", (cfg.T, cfg.K), torch.float32, dev)
+    rc = (_lib or lib()).moe_rows_unsort_grad(cfg.c(ld, ld_s, 0, ld_d), dy_ptr, ys_ptr, gate_ptr, pos_ptr, dys_ptr,
+                                              dgate_ptr, ws_ptr, raw_stream(dev))
     if rc:
         raise moe.MoeError(rc, "moe_rows_unsort_grad")
     return dys, dgate
