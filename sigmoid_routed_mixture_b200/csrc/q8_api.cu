@@ -42,6 +42,11 @@ moe_status_t run_rows(const moe_q8_rows_t *cfg, const void *x, const void *delta
       (y && !good_ld(cfg->ld_y, cfg->H)))
     return MOE_ERR_ARG;
   if (y && y == x_sum) return MOE_ERR_ARG;  // two results in one place
+  // a result in an input's place has its rows where the input has them
+  auto same_rows = [&](const void *out, int64_t ld_out) {
+    return !out || cfg->T < 2 || ((out != x || ld_out == cfg->ld_x) && (out != delta || ld_out == cfg->ld_delta));
+  };
+  if (!same_rows(x_sum, cfg->ld_sum) || !same_rows(y, cfg->ld_y)) return MOE_ERR_ARG;
   const size_t e = dtype_size(cfg->dtype);
   const void *ptrs[] = {x, delta, gamma, x_sum, y};
   for (const void *p : ptrs)
@@ -72,7 +77,7 @@ moe_status_t check_matmul(const moe_q8_matmul_t *c) {
   if (c->R < 0 || c->N < 1 || c->K < 1 || c->groups < 1 || !float_dtype(c->dtype)) return MOE_ERR_ARG;
   if (c->swiglu != 0 && c->swiglu != 1) return MOE_ERR_ARG;
   if (c->K % 16 != 0 || c->K > 65536 || (c->swiglu && c->N % 32 != 0)) return MOE_ERR_UNSUPPORTED;
-  if (c->groups > srm::kQ8MaxGroups || c->R >= (int64_t(1) << 31) ||
+  if (c->groups > srm::kQ8MaxGroups || c->R >= (int64_t(1) << 31) - 1024 ||
       static_cast<int64_t>(c->groups) * c->N >= (int64_t(1) << 31))
     return MOE_ERR_UNSUPPORTED;
   // tile numbers are 32-bit
@@ -125,7 +130,8 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
   if (residual && cfg->swiglu) return MOE_ERR_ARG;
   const int64_t cols = cfg->swiglu ? cfg->N / 2 : cfg->N;
   if (!good_ld(cfg->ld_x, cfg->K) || !good_ld(cfg->ld_y, cols) ||
-      (residual && !good_ld(cfg->ld_residual, cols)))
+      (residual && !good_ld(cfg->ld_residual, cols)) ||
+      (residual == y && cfg->R > 1 && cfg->ld_residual != cfg->ld_y))
     return MOE_ERR_ARG;
   const size_t e = dtype_size(cfg->dtype);
   if (!aligned(x, 16) || cfg->ld_x % 16 != 0 || !aligned(w, 16) || !aligned(x_scale, 4) ||

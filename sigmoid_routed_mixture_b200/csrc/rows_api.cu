@@ -75,7 +75,8 @@ moe_status_t moe_rows_unsort(const moe_rows_cfg_t *cfg, const void *ys, const fl
   if (st != MOE_OK || cfg->T == 0) return st;
   if (!ys || !pos || !y || !ws) return MOE_ERR_ARG;
   if (!good_ld(cfg, cfg->ld_token) || !good_ld(cfg, cfg->ld_slot) ||
-      (residual && !good_ld(cfg, cfg->ld_residual)))
+      (residual && !good_ld(cfg, cfg->ld_residual)) ||
+      (residual == y && cfg->T > 1 && cfg->ld_residual != cfg->ld_token))
     return MOE_ERR_ARG;
   const size_t e = dtype_size(cfg->dtype);
   if (!aligned(ys, dtype_size(cfg->slot_dtype)) || (gate && !aligned(gate, 4)) || !aligned(pos, 4) ||
@@ -101,7 +102,7 @@ moe_status_t moe_rows_unsort_grad(const moe_rows_cfg_t *cfg, const void *dy, con
   if (st != MOE_OK || cfg->T == 0) return st;
   if (!dy || !pos || !ws || (!dys && !dgate) || (dgate && !ys)) return MOE_ERR_ARG;
   if (!good_ld(cfg, cfg->ld_token) || (dgate && !good_ld(cfg, cfg->ld_slot)) ||
-      (dys && !good_ld(cfg, cfg->ld_dys)))
+      (dys && !good_ld(cfg, cfg->ld_dys)) || (dys && dgate && dys == ys && cfg->ld_dys != cfg->ld_slot))
     return MOE_ERR_ARG;
   const size_t es = dtype_size(cfg->slot_dtype);
   if (!aligned(dy, dtype_size(cfg->dtype)) || (ys && !aligned(ys, es)) || (gate && !aligned(gate, 4)) ||

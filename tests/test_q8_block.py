@@ -174,3 +174,24 @@ def test_dense_mlp(T, H, I):
     with pytest.raises(ValueError):
         ffn(torch.cat([x, x]))
     assert ffn.device_error() == 0
+
+
+def test_empty_batch_and_ids_out_of_range():
+    cfg, blk, w, g = block(0, 4, 2, 256, 128, True, 5)
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
+    assert blk(x).shape == (0, 256) and blk.device_error() == 0
+    ffn = q8.DenseMlp(moe.Config.dense(8, 256, 128), w["ws1"], w["ws3"], w["ws2"])
+    assert ffn(x).shape == (0, 256) and ffn.device_error() == 0
+    # rows that are not finite come out not finite, and leave the others alone
+    cfg, blk, w, g = block(64, 4, 2, 256, 128, True, 6)
+    x = torch.randn(64, 256, generator=g, device="cuda").to(torch.bfloat16)
+    good = blk(x).clone()
+    gamma = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    sub = blk.sublayer(x, gamma)[0].clone()
+    x[7, 3] = float("inf")
+    x[9, 0] = float("nan")
+    bad = blk.sublayer(x, gamma)[0]
+    rest = [r for r in range(64) if r not in (7, 9)]
+    assert torch.equal(bad[rest], sub[rest]) and torch.isnan(bad[[7, 9]]).all()
+    x[7, 3] = x[9, 0] = 0
+    assert not torch.isnan(good).any()

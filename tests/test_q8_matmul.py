@@ -50,6 +50,7 @@ def test_pointers_refused():
         assert call(c, **{bad: odd}) == 3, bad
     assert call(c_cfg(ld_x=72)) == 3  # rows off 16 bytes
     assert call(c_cfg(ld_x=48)) == 1 and call(c_cfg(ld_y=63)) == 1 and call(c_cfg(ld_r=63), res=A) == 1
+    assert call(c_cfg(ld_r=72), res=A) == 1  # in place, its rows elsewhere
     assert call(c_cfg(groups=2), off=None) == 1
     assert call(c_cfg(swiglu=1), res=A) == 1
     need = q8.lib().moe_q8_matmul_workspace_size(ctypes.byref(c))

@@ -50,6 +50,12 @@ def test_row_pointers_refused():
     assert L.moe_q8_add_rmsnorm(c, A, A, A, -1e-5, A, None, A, A, None) == 1
     assert L.moe_q8_add_rmsnorm(c, A, A, A, float("nan"), A, None, A, A, None) == 1
     assert L.moe_q8_add_rmsnorm(c, A, A, A, 1e-5, B2, B2, A, A, None) == 1  # sum and norm in one place
+    apart = rows_cfg()
+    apart.ld_y = 72  # a result in an input's place, its rows elsewhere
+    assert L.moe_q8_add_rmsnorm(ctypes.byref(apart), A, B2, A, 1e-5, None, A, B2, B2, None) == 1
+    assert L.moe_q8_add_rmsnorm(ctypes.byref(apart), B2, A, A, 1e-5, None, A, B2, B2, None) == 1
+    apart.ld_sum = 72
+    assert L.moe_q8_add_rmsnorm(ctypes.byref(apart), A, B2, A, 1e-5, A, None, B2, B2, None) == 1
     assert L.moe_q8_add_rmsnorm(c, ODD, A, A, 1e-5, A, None, A, A, None) == 3
     assert L.moe_q8_add_rmsnorm(c, A, A, A, 1e-5, A, ODD, A, A, None) == 3
     assert L.moe_q8_add_rmsnorm(c, A, A, A, 1e-5, A, None, A, ODD, None) == 3

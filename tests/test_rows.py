@@ -60,6 +60,10 @@ def test_types_and_pointers_refused():
     assert L.moe_rows_unsort_grad(c, A, A, A, A, None, None, A, None) == 1
     assert L.moe_rows_unsort_grad(c, A, None, A, A, A, A, A, None) == 1
     assert L.moe_rows_unsort_grad(c, A, A, A, A, ODD, A, A, None) == 3
+    apart = c_cfg()
+    apart.ld_residual = apart.ld_dys = 72  # in place, their rows elsewhere
+    assert L.moe_rows_unsort(ctypes.byref(apart), A, A, A, A, A, A, None) == 1
+    assert L.moe_rows_unsort_grad(ctypes.byref(apart), A, A, A, A, A, A, A, None) == 1
     empty = ctypes.byref(c_cfg(T=0))
     assert L.moe_rows_sort(empty, *[None] * 9) == 0 and L.moe_rows_unsort(empty, *[None] * 7) == 0
     assert L.moe_rows_sort_grad(empty, *[None] * 5) == 0 and L.moe_rows_unsort_grad(empty, *[None] * 8) == 0
@@ -221,11 +225,13 @@ def test_strides(ld, offset):
 
 
 @pytest.mark.gpu
-def test_after_permute_with_ids_out_of_range():
+@pytest.mark.parametrize("T", [300, 900])  # the inverse in one launch, and in several
+def test_after_permute_with_ids_out_of_range(T):
     """moe_permute skips and flags an id out of range: its assignment has no row, and adds nothing."""
-    T, H, E, K = 300, 256, 16, 4
+    H, E, K = 256, 16, 4
     block = moe.Config(T=T, H=H, I=128, E=E, K=K)
     cfg = rows.Config.of(block)
+    assert (cfg.rows <= 4096) == (T == 300)
     idx = torch.rand(T, E, generator=gen(7), device="cuda").argsort(1)[:, :K].to(torch.int32).contiguous()
     idx[3, 1], idx[200, 0], idx[299] = -1, E, 1000
     ws = moe.workspace(block)
@@ -251,8 +257,9 @@ def test_after_permute_with_ids_out_of_range():
 
 
 @pytest.mark.gpu
-def test_bad_ids_and_positions_are_flagged():
-    T, H, E, K = 20, 32, 4, 2
+@pytest.mark.parametrize("T", [20, 2000])  # the inverse in one launch, and in several
+def test_bad_ids_and_positions_are_flagged(T):
+    H, E, K = 32, 4, 2
     cfg = rows.Config(T, H, E, K)
     gate, offsets, ids, pos = routing(T, E, K, True, 11)
     x = torch.randn(T, H, generator=gen(12), device="cuda").to(torch.bfloat16)
