@@ -197,7 +197,11 @@ struct Q8Plan {
 };
 Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms);
 int64_t q8_partials(int64_t R, int num_sms);  // int32 partial sums in the workspace
-cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const TokMaps &tok, const CUtensorMap &tw,
-                           const Q8GemmArgs &p, int num_sms, cudaStream_t stream);
+// x with boxes of 32, 64 and 128 rows, w with boxes of 128 rows
+struct Q8Maps {
+  CUtensorMap tok[3], w;
+};
+cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const Q8Maps &tmaps, const Q8GemmArgs &p,
+                           int num_sms, cudaStream_t stream);
 
 }  // namespace srm

@@ -142,14 +142,11 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
   if (ws_bytes < matmul_ws_bytes(cfg->R)) return MOE_ERR_WORKSPACE;
   uint8_t *wsb = static_cast<uint8_t *>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  srm::TokMaps tok;
-  CUtensorMap tw;
+  srm::Q8Maps maps;
   const uint64_t K = cfg->K, R = cfg->R, pitch = cfg->ld_x;
-  if (!make_tmap_8bit(&tok.small, x, K, R, pitch, static_cast<uint32_t>(srm::gemm_tok_box_rows())) ||
-      !make_tmap_8bit(&tok.big, x, K, R, pitch, static_cast<uint32_t>(srm::gemm_tok_big_box_rows())) ||
-      !make_tmap_8bit(&tw, w, K, static_cast<uint64_t>(cfg->groups) * cfg->N, K,
-                      static_cast<uint32_t>(srm::gemm_w_box_rows())))
-    return MOE_ERR_CUDA;
+  bool ok = make_tmap_8bit(&maps.w, w, K, static_cast<uint64_t>(cfg->groups) * cfg->N, K, 128);
+  for (int i = 0; i < 3; ++i) ok = ok && make_tmap_8bit(&maps.tok[i], x, K, R, pitch, 32u << i);
+  if (!ok) return MOE_ERR_CUDA;
   srm::Q8GemmArgs p = {};
   p.x_scale = x_scale;
   p.w_scale = w_scale;
@@ -172,7 +169,7 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
   p.max_mtiles = static_cast<int>(plan.max_mtiles);
   const char *inject = getenv("SRM_MOE_INJECT_STALL");
   p.stall = (inject && inject[0] == '1') ? 1 : 0;
-  return cuda_status(srm::launch_q8_gemm(cfg->swiglu != 0, cfg->dtype, plan.pair, tok, tw, p, num_sms(), s));
+  return cuda_status(srm::launch_q8_gemm(cfg->swiglu != 0, cfg->dtype, plan.pair, maps, p, num_sms(), s));
 }
 
 moe_status_t moe_q8_add_rmsnorm(const moe_q8_rows_t *cfg, const void *x, const void *delta,

@@ -39,8 +39,6 @@ namespace srm {
 namespace q8 {
 constexpr int BM = 128;           // weight rows per CTA (tensor-memory lanes)
 constexpr int BK = 128;           // elements (bytes) of K per step: one swizzle atom
-constexpr int TOK_BOX = 32;       // token rows per TMA box of a tail tile
-constexpr int TOK_BOX_BIG = 128;  // ... of a full tile
 constexpr int EPI_WARPS = kQ8EpiWarps;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int MAX_GROUPS = kQ8MaxGroups;
@@ -109,6 +107,36 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64
       "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// A box of a tensor map to shared memory, completion counted on the mbarrier at
+// `bar` (the leader's, for a pair; no multicast).
+template <bool kPair>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *tmap, uint32_t bar, int32_t c0,
+                                          int32_t c1) {
+  if (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
 }
 
 struct Tile {
@@ -228,8 +256,7 @@ __device__ __forceinline__ float silu<float>(float g) {
 }
 
 template <bool kSwiglu, bool kPair, typename T>
-__device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUtensorMap &tmap_tok_big,
-                                          const CUtensorMap &tmap_w, const Q8GemmArgs &p) {
+__device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs &p) {
   using C = Cfg<kPair>;
   constexpr int BT = C::BT;
   constexpr uint32_t TMEM_COLS = C::TMEM_COLS;
@@ -271,9 +298,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
     s.abort_flag = 0;
     s.mma_consumed = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tmap_tok);
-    tma_prefetch_desc(&tmap_tok_big);
-    tma_prefetch_desc(&tmap_w);
+    for (int i = 0; i < 3; ++i) tma_prefetch_desc(&tmaps.tok[i]);
+    tma_prefetch_desc(&tmaps.w);
   }
   if (warp == 1) {
     if (kPair) {
@@ -353,6 +379,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
     // while another is idle, early enough to hide the counter's round trip and
     // the signal to the peer.  (Two ids drawn ahead left 28 of 148 CTAs
     // without work, and 24 with two tiles, at 144 tiles.)
+    const bool elected = elect_one();
+    const uint32_t a_smem = smem_addr(sA), b_smem = smem_addr(sB);
+    // a pair's loads all complete on the leader's barriers
+    const uint32_t full0 = kPair ? cluster_map(&s.full[0], 0) : smem_addr(&s.full[0]);
     uint32_t stage = 0, phase = 0, ts = 0, tph = 0;
     uint32_t ps = 0, pph = 0;  // next ring slot to publish and its phase
     const int stride = static_cast<int>(gridDim.x) / C::RANKS;
@@ -404,11 +434,11 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
       const int w_row = c.g * p.N + c.w0 + static_cast<int>(rank) * BM;
       const int tok_rows = kPair ? c.n / 2 : c.n;
       const int tok_row0 = c.row_base + static_cast<int>(rank) * tok_rows;
-      const bool big = tok_rows % TOK_BOX_BIG == 0;
-      const int box_rows = big ? TOK_BOX_BIG : TOK_BOX;
-      const CUtensorMap *tmap_b = big ? &tmap_tok_big : &tmap_tok;
-      const int nb = (tok_rows + box_rows - 1) / box_rows;
-      const uint32_t tx = (kPair ? 2u : 1u) * static_cast<uint32_t>(A_BYTES + nb * box_rows * BK);
+      // one box of 32, 64 or 128 rows holds this CTA's token rows: each TMA
+      // instruction costs issue time on the one producing lane
+      const int box = tok_rows <= 32 ? 0 : tok_rows <= 64 ? 1 : 2;
+      const CUtensorMap *tmap_b = &tmaps.tok[box];
+      const uint32_t tx = (kPair ? 2u : 1u) * static_cast<uint32_t>(A_BYTES + (32 << box) * BK);
       const int draw_at = max(c.kb0, c.kb1 - STAGES);
       for (int kb = c.kb0; kb < c.kb1; ++kb) {
         if (leader && !streamed && kb == draw_at && !publish(true)) {
@@ -419,21 +449,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (elected) {
           if (leader) mbar_arrive_expect_tx(&s.full[stage], tx);
-          uint8_t *b_dst = sB + stage * B_BYTES;
-          if (kPair) {
-            const uint32_t full_leader = cluster_map(&s.full[stage], 0);
-            tma_load_2d_pair(sA + stage * A_BYTES, &tmap_w, full_leader, kb * BK, w_row);
-            for (int j = 0; j < nb; ++j)
-              tma_load_2d_pair(b_dst + j * box_rows * BK, tmap_b, full_leader, kb * BK,
-                               tok_row0 + j * box_rows);
-          } else {
-            tma_load_2d(sA + stage * A_BYTES, &tmap_w, &s.full[stage], kb * BK, w_row);
-            for (int j = 0; j < nb; ++j)
-              tma_load_2d(b_dst + j * box_rows * BK, tmap_b, &s.full[stage], kb * BK,
-                          tok_row0 + j * box_rows);
-          }
+          load_tile<kPair>(a_smem + stage * A_BYTES, &tmaps.w, full0 + stage * 8, kb * BK, w_row);
+          load_tile<kPair>(b_smem + stage * B_BYTES, tmap_b, full0 + stage * 8, kb * BK, tok_row0);
         }
         __syncwarp();
         ++issued;
@@ -446,6 +465,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (leader) {
+      const bool elected = elect_one();
+      const uint64_t a_desc0 = umma_desc_sw128(smem_addr(sA)), b_desc0 = umma_desc_sw128(smem_addr(sB));
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, ts = 0, tph = 0;
       int consumed = 0;
       while (true) {
@@ -473,18 +494,16 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
           }
           tc_fence_after();
           ++consumed;
-          if (lane == 0) {
-            const uint32_t a_addr = smem_addr(sA + stage * A_BYTES);
-            const uint32_t b_addr = smem_addr(sB + stage * B_BYTES);
+          if (elected) {
+            // a step of 32 bytes of K adds 2 to a descriptor's address field
+            const uint64_t a_desc = a_desc0 + stage * (A_BYTES >> 4), b_desc = b_desc0 + stage * (B_BYTES >> 4);
 #pragma unroll
             for (int k = 0; k < BK / 32; ++k) {
               const uint32_t accumulate = kb != c.kb0 || k != 0 ? 1u : 0u;
               if (kPair)
-                mma_pair(d_tmem, umma_desc_sw128(a_addr + k * 32), umma_desc_sw128(b_addr + k * 32), idesc,
-                         accumulate);
+                mma_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
               else
-                mma(d_tmem, umma_desc_sw128(a_addr + k * 32), umma_desc_sw128(b_addr + k * 32), idesc,
-                    accumulate);
+                mma(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
             }
             if (kPair)
               umma_commit_pair(&s.empty[stage], 0x3);
@@ -498,7 +517,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
           }
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (elected) {
           if (kPair)
             umma_commit_pair(&s.tfull[acc], 0x3);
           else
@@ -733,18 +752,14 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmap_tok, const CUt
 
 template <bool kSwiglu, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    q8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_tok,
-                        const __grid_constant__ CUtensorMap tmap_tok_big,
-                        const __grid_constant__ CUtensorMap tmap_w, Q8GemmArgs p) {
-  gemm_body<kSwiglu, true, T>(tmap_tok, tmap_tok_big, tmap_w, p);
+    q8_gemm_pair_kernel(const __grid_constant__ Q8Maps tmaps, Q8GemmArgs p) {
+  gemm_body<kSwiglu, true, T>(tmaps, p);
 }
 
 template <bool kSwiglu, typename T>
 __global__ void __launch_bounds__(THREADS, 1)
-    q8_gemm_solo_kernel(const __grid_constant__ CUtensorMap tmap_tok,
-                        const __grid_constant__ CUtensorMap tmap_tok_big,
-                        const __grid_constant__ CUtensorMap tmap_w, Q8GemmArgs p) {
-  gemm_body<kSwiglu, false, T>(tmap_tok, tmap_tok_big, tmap_w, p);
+    q8_gemm_solo_kernel(const __grid_constant__ Q8Maps tmaps, Q8GemmArgs p) {
+  gemm_body<kSwiglu, false, T>(tmaps, p);
 }
 
 // As many CTA pairs as can be resident at once (the kernel is persistent), and
@@ -774,8 +789,7 @@ cudaError_t prepare_kernel(Kern kern, size_t smem, bool pair, int num_sms, int *
 }
 
 template <bool kSwiglu, typename T>
-cudaError_t launch_t(const TokMaps &tok, const CUtensorMap &tw, const Q8GemmArgs &p, bool pair, int num_sms,
-                     cudaStream_t stream) {
+cudaError_t launch_t(const Q8Maps &tmaps, const Q8GemmArgs &p, bool pair, int num_sms, cudaStream_t stream) {
   static int cached[2][64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -787,23 +801,23 @@ cudaError_t launch_t(const TokMaps &tok, const CUtensorMap &tw, const Q8GemmArgs
     e = prepare_kernel(kern, smem, true, num_sms, &resident);
     if (e != cudaSuccess) return e;
     return launch_overlapped(kern, 2 * static_cast<unsigned>(p.units < resident ? p.units : resident), THREADS, smem,
-                             stream, tok.small, tok.big, tw, p);
+                             stream, tmaps, p);
   }
   auto kern = q8_gemm_solo_kernel<kSwiglu, T>;
   constexpr size_t smem = smem_bytes<false>();
   e = prepare_kernel(kern, smem, false, num_sms, &resident);
   if (e != cudaSuccess) return e;
   return launch_overlapped(kern, static_cast<unsigned>(p.units < resident ? p.units : resident), THREADS, smem,
-                           stream, tok.small, tok.big, tw, p);
+                           stream, tmaps, p);
 }
 }  // namespace q8
 
-cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const TokMaps &tok, const CUtensorMap &tw,
-                           const Q8GemmArgs &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const Q8Maps &tmaps, const Q8GemmArgs &p,
+                           int num_sms, cudaStream_t stream) {
   auto go = [&](auto t) {
     using T = decltype(t);
-    return swiglu ? q8::launch_t<true, T>(tok, tw, p, pair, num_sms, stream)
-                  : q8::launch_t<false, T>(tok, tw, p, pair, num_sms, stream);
+    return swiglu ? q8::launch_t<true, T>(tmaps, p, pair, num_sms, stream)
+                  : q8::launch_t<false, T>(tmaps, p, pair, num_sms, stream);
   };
   if (dtype == MOE_DTYPE_BF16) return go(Bf16{});
   if (dtype == MOE_DTYPE_FP16) return go(Fp16{});
