@@ -92,7 +92,7 @@ moe_status_t moe_q8_pack_weights(const moe_cfg_t *cfg, const void *w1, const voi
  *   swiglu: 0, or 1: the channels are units of 16 gate and the 16 matching up
  *           channels (moe_q8_pack_weights' w13; N % 32 == 0) and the result is
  *           silu(gate) * up, N / 2 columns
- *   dtype:  of y and residual: BF16, FP16 (beyond +-65504 saturated and flagged
+ *   dtype:  of y and residual: BF16, FP16 (past +-65504 saturated and flagged
  *           MOE_ERR_RANGE on the device), FP32
  *   ld_x, ld_y, ld_residual: row strides in elements; ld_x % 16 == 0. */
 typedef struct {

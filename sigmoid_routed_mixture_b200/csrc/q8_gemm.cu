@@ -230,18 +230,47 @@ struct Stream {
   }
 };
 
-// Results to their type: fp16 saturates at +-65504 (flagged at the end by the
-// largest magnitude seen), as the library's other fp16 intermediates do; NaN
-// stays NaN.
+// Two results (of two rows) in their type.  fp16 saturates at +-65504, as the
+// library's other fp16 intermediates do: an infinity becomes the largest finite
+// number, `largest` keeps the largest magnitudes seen for the flag; NaN stays.
 template <typename T>
-__device__ __forceinline__ float fit(float v, float &largest) {
-  return v;
+struct Pair2 {
+  T lo, hi;
+};
+template <typename T>
+__device__ __forceinline__ Pair2<T> to_pair(float a, float b, uint32_t &largest) {
+  const uint32_t w = pack2<T>(a, b);
+  return {T{static_cast<uint16_t>(w)}, T{static_cast<uint16_t>(w >> 16)}};
 }
 template <>
-__device__ __forceinline__ float fit<Fp16>(float v, float &largest) {
-  largest = fmaxf(largest, fabsf(v));
-  asm("max.NaN.f32 %0, %0, 0fC77FE000;\n\tmin.NaN.f32 %0, %0, 0f477FE000;" : "+f"(v));
-  return v;
+__device__ __forceinline__ Pair2<float> to_pair<float>(float a, float b, uint32_t &largest) {
+  return {a, b};
+}
+template <>
+__device__ __forceinline__ Pair2<Fp16> to_pair<Fp16>(float a, float b, uint32_t &largest) {
+  uint32_t w = pack2<Fp16>(a, b);
+  asm("{\n\t.reg .b32 m;\n\t"
+      "abs.f16x2 m, %0;\n\t"
+      "max.f16x2 %1, %1, m;\n\t"
+      "min.NaN.f16x2 %0, %0, %2;\n\t"
+      "max.NaN.f16x2 %0, %0, %3;\n\t}"
+      : "+r"(w), "+r"(largest)
+      : "r"(0x7bff7bffu), "r"(0xfbfffbffu));
+  return {Fp16{static_cast<uint16_t>(w)}, Fp16{static_cast<uint16_t>(w >> 16)}};
+}
+__device__ __forceinline__ bool saturated(uint32_t largest) {  // an infinity in either half
+  return (largest & 0x7fffu) == 0x7c00u || (largest >> 16 & 0x7fffu) == 0x7c00u;
+}
+
+// (a, b) * (c, d) in one operation
+__device__ __forceinline__ void mul2(float &a, float &b, float c, float d) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
 }
 
 // silu for results of 16 bits from the hardware approximations (relative error
@@ -614,7 +643,7 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
         mine = __shfl_sync(0xffffffffu, seen, 0) == last_unit - first_unit;
         __threadfence();
       }
-      float largest = 0.f;
+      uint32_t largest = 0;
       if (mine) {
         for (int m = m_first; 32 * m < c.n; m += STEP) {
           const int64_t row0 = c.row_base + 32 * m;
@@ -636,10 +665,12 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
             const float4 xs = *reinterpret_cast<const float4 *>(&row_scale[32 * m + k]);
-            v[k] = static_cast<float>(static_cast<int32_t>(cv[k])) * ws * xs.x;
-            v[k + 1] = static_cast<float>(static_cast<int32_t>(cv[k + 1])) * ws * xs.y;
-            v[k + 2] = static_cast<float>(static_cast<int32_t>(cv[k + 2])) * ws * xs.z;
-            v[k + 3] = static_cast<float>(static_cast<int32_t>(cv[k + 3])) * ws * xs.w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[k + e] = static_cast<float>(static_cast<int32_t>(cv[k + e]));
+            mul2(v[k], v[k + 1], ws, ws);
+            mul2(v[k + 2], v[k + 3], ws, ws);
+            mul2(v[k], v[k + 1], xs.x, xs.y);
+            mul2(v[k + 2], v[k + 3], xs.z, xs.w);
           }
           if (kSwiglu) {
             // lanes 0-15 hold the gate channels of 16 features, lanes 16-31 the
@@ -647,21 +678,31 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
             // high lanes the second
             const bool high = lane >= 16;
             T *y = static_cast<T *>(p.y) + (row0 + high) * p.ld_y + wr / 2 + (lane & 15);
-            T out[16];
+            float h[16];
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               const float got = __shfl_xor_sync(0xffffffffu, high ? v[k] : v[k + 1], 16);
               const float gate = high ? got : v[k], up = high ? v[k + 1] : got;
-              const float h = silu<T>(gate) * up;
-              out[k / 2] = from_float<T>(fit<T>(h, largest));
+              h[k / 2] = silu<T>(gate) * up;
             }
             if (live == 32) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k, y += 2 * p.ld_y) *y = out[k];
+              for (int k = 0; k < 16; k += 2) {
+                const Pair2<T> out = to_pair<T>(h[k], h[k + 1], largest);
+                *y = out.lo;
+                y += 2 * p.ld_y;
+                *y = out.hi;
+                y += 2 * p.ld_y;
+              }
             } else {
 #pragma unroll
-              for (int k = 0; k < 16; ++k, y += 2 * p.ld_y)
-                if (2 * k + high < live) *y = out[k];
+              for (int k = 0; k < 16; k += 2) {
+                const Pair2<T> out = to_pair<T>(h[k], h[k + 1], largest);
+                if (2 * k + high < live) *y = out.lo;
+                y += 2 * p.ld_y;
+                if (2 * k + 2 + high < live) *y = out.hi;
+                y += 2 * p.ld_y;
+              }
             }
           } else if (inside) {
             if (add) {
@@ -678,18 +719,28 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
             T *y = static_cast<T *>(p.y) + row0 * p.ld_y + ch;
             if (live == 32) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k, y += p.ld_y) *y = from_float<T>(fit<T>(v[k], largest));
+              for (int k = 0; k < 32; k += 2) {
+                const Pair2<T> out = to_pair<T>(v[k], v[k + 1], largest);
+                *y = out.lo;
+                y += p.ld_y;
+                *y = out.hi;
+                y += p.ld_y;
+              }
             } else {
 #pragma unroll
-              for (int k = 0; k < 32; ++k, y += p.ld_y) {
+              for (int k = 0; k < 32; k += 2) {
                 if (k >= live) break;
-                *y = from_float<T>(fit<T>(v[k], largest));
+                const Pair2<T> out = to_pair<T>(v[k], v[k + 1], largest);
+                *y = out.lo;
+                y += p.ld_y;
+                if (k + 1 < live) *y = out.hi;
+                y += p.ld_y;
               }
             }
           }
         }
       }
-      if (largest > 65504.f) record_error(p.err, MOE_ERR_RANGE);
+      if (saturated(largest)) record_error(p.err, MOE_ERR_RANGE);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -831,11 +882,13 @@ cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const Q8Maps &tmap
 //   holds at most 64 rows (64 x 24576 x 6144: 38 us against 42), and while all
 //   their tiles run at once (777 x 1001 x 2064: 14 against 19 us); pairs above
 //   (256 x 6144 x 12288: 40 against 53).
-//   Streamed shares while the tiles do not fill the units twice.  With no more
-//   tiles than units each tile is cut into equal parts, so many that a further
-//   one would cost more (about 2 us of exchange for single CTAs, 6 for pairs)
-//   than its share of the tile's k-blocks; otherwise the shares straddle tiles
-//   (1 x 24576 x 6144, 192 tiles: 33 us against 38 dealt out whole).
+//   Streamed with no more tiles than units: each tile is cut into equal parts,
+//   so many that a further one would cost more (about 2 us of exchange for
+//   single CTAs, 6 for pairs) than its share of the tile's k-blocks.  Single
+//   CTAs also up to twice as many tiles, their shares then straddling tiles
+//   (1 x 24576 x 6144, 192 tiles: 33 us against 38 dealt out whole); for pairs
+//   the exchange costs more than the uneven end (4096 x 2048 x 1536, 128 tiles:
+//   40 us against 19).
 Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms) {
   Q8Plan p;
   const int64_t touched = R < groups ? R : groups;
@@ -847,7 +900,7 @@ Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms) {
   p.max_mtiles = blocks(bt);
   const int64_t tiles = p.max_mtiles * ((N + wb - 1) / wb);
   const int64_t kblocks = (K + 127) / 128;
-  p.streamed = tiles < 2 * units;
+  p.streamed = tiles <= units || (!p.pair && tiles < 2 * units);
   p.units = tiles < units ? static_cast<int>(tiles) : units;
   if (tiles > 0 && tiles <= units) {
     const int64_t cost = p.pair ? 21 : 7;  // k-blocks' time that a further part costs
