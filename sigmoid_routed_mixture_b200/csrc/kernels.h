@@ -187,12 +187,13 @@ struct Q8GemmArgs {
   int R, N, K, groups;
   int streamed;            // the tiles' k-blocks in equal shares (few tiles), or whole tiles
   int units;               // CTAs (or pairs) that the work is for
+  int max_parts;           // streamed: parts a tile may be cut into
   int max_mtiles;          // token blocks the workspace is laid out for
   int stall;               // failure-detection tests only: the producer issues no loads
 };
 struct Q8Plan {
   bool pair, streamed;
-  int units;
+  int units, max_parts;
   int64_t max_mtiles;
 };
 Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms);

@@ -166,6 +166,7 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
   p.groups = cfg->groups;
   p.streamed = plan.streamed;
   p.units = plan.units;
+  p.max_parts = plan.max_parts;
   p.max_mtiles = static_cast<int>(plan.max_mtiles);
   const char *inject = getenv("SRM_MOE_INJECT_STALL");
   p.stall = (inject && inject[0] == '1') ? 1 : 0;

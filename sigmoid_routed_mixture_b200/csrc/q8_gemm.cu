@@ -204,9 +204,13 @@ __device__ __forceinline__ bool ring_tile(const Smem &s, uint32_t ts, int kblock
 struct Stream {
   int64_t total, pos, end;
   int units, kblocks;
-  __device__ __forceinline__ Stream(int64_t tiles, int kblocks_, int units_, int unit)
+  // With no more tiles than units, every tile in equal parts: the number of
+  // tiles is only known here, a group's rows being the device's to know.
+  // Otherwise the shares straddle tiles.  No share is empty either way.
+  __device__ __forceinline__ Stream(int64_t tiles, int kblocks_, int units_, int max_parts, int unit)
       : total(tiles * kblocks_), pos(0), end(0), units(units_), kblocks(kblocks_) {
-    if (total < units) units = static_cast<int>(total);  // no share is empty
+    if (tiles > 0 && tiles <= units)
+      units = static_cast<int>(tiles * min(min(max_parts, kblocks), static_cast<int>(units / tiles)));
     if (unit < units) {
       pos = begin(unit);
       end = begin(unit + 1);
@@ -395,7 +399,7 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
   const int total_tiles = s.total_mtiles * n_tiles;
   const bool counted = s.ready != 0;
   const bool streamed = p.streamed && counted;
-  Stream stream(total_tiles, kblocks, static_cast<int>(gridDim.x) / C::RANKS,
+  Stream stream(total_tiles, kblocks, static_cast<int>(gridDim.x) / C::RANKS, p.max_parts,
                 static_cast<int>(blockIdx.x) / C::RANKS);
   volatile int *abort_flag = &s.abort_flag;
   int issued = 0;  // k-blocks this CTA's producer has loaded
@@ -902,12 +906,11 @@ Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms) {
   const int64_t kblocks = (K + 127) / 128;
   p.streamed = tiles <= units || (!p.pair && tiles < 2 * units);
   p.units = tiles < units ? static_cast<int>(tiles) : units;
-  if (tiles > 0 && tiles <= units) {
-    const int64_t cost = p.pair ? 21 : 7;  // k-blocks' time that a further part costs
-    int64_t parts = 1;
-    while ((parts + 1) * parts * cost <= kblocks && (parts + 1) * tiles <= units) ++parts;
-    p.units = static_cast<int>(parts * tiles);
-  }
+  const int64_t cost = p.pair ? 21 : 7;  // k-blocks' time that a further part costs
+  p.max_parts = 1;
+  while ((p.max_parts + 1) * p.max_parts * cost <= kblocks) ++p.max_parts;
+  if (tiles > 0 && tiles <= units)
+    p.units = static_cast<int>(tiles * (p.max_parts * tiles <= units ? p.max_parts : units / tiles));
   return p;
 }
 
