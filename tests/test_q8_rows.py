@@ -129,7 +129,7 @@ def check(x, n, q, scale, y=None, normed=True):
 
 
 SHAPES = [(1, 1), (1, 6144), (3, 64), (5, 257), (7, 1541), (2, 4097), (300, 2048), (301, 1000), (1000, 8), (2, 40008),
-          (400, 6144)]
+          (400, 6144), (2, 9311), (3, 16391), (2, 30000), (301, 4097)]
 
 
 @pytest.mark.gpu
