@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(256)
     rows_unsort_grad_kernel(const RowsArgs p, const Tt *__restrict__ dy, const Ts *ys,
                             const float *__restrict__ gate, const int32_t *__restrict__ pos, Ts *dys,
                             float *dgate, int wpt) {
-  constexpr int B = 4;
+  constexpr int B = E == 1 ? 16 : 4;
   __shared__ float partial[8][16];
   previous_done();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
