@@ -13,11 +13,14 @@
 
 namespace srm {
 
-// Every block of a grid says that the next kernel may be set up (it has all its
-// resources by then) before it waits for the previous one.
-__device__ __forceinline__ void previous_done() {
-  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-}
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next kernel be set up before this one ends (without it, as this
+// one's blocks end).  Worth it where a block holds an SM to itself (the 8-bit
+// products: 32.8 -> 32.0 us at 1 x 24576 x 6144); kernels of many small blocks
+// lose (64 tokens to the experts 4.5 -> 5.5 us), the next one's taking their
+// places.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... Params, typename... Args>
 cudaError_t launch_overlapped(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,

@@ -343,6 +343,7 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
       tmem_relinquish();
     }
   }
+  let_next_start();
   previous_done();
   if (threadIdx.x == 64) s.ready = *p.ready == kQ8Ready;
   if (warp == 0) {
