@@ -209,8 +209,9 @@ struct Stream {
   // Otherwise the shares straddle tiles.  No share is empty either way.
   __device__ __forceinline__ Stream(int64_t tiles, int kblocks_, int units_, int max_parts, int unit)
       : total(tiles * kblocks_), pos(0), end(0), units(units_), kblocks(kblocks_) {
-    if (tiles > 0 && tiles <= units)
-      units = static_cast<int>(tiles * min(min(max_parts, kblocks), static_cast<int>(units / tiles)));
+    if (tiles == 0) return;
+    if (tiles <= units)
+      units = static_cast<int>(tiles * min(min(max_parts, kblocks), units / static_cast<int>(tiles)));
     if (unit < units) {
       pos = begin(unit);
       end = begin(unit + 1);
@@ -400,7 +401,7 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
   const int total_tiles = s.total_mtiles * n_tiles;
   const bool counted = s.ready != 0;
   const bool streamed = p.streamed && counted;
-  Stream stream(total_tiles, kblocks, static_cast<int>(gridDim.x) / C::RANKS, p.max_parts,
+  Stream stream(streamed ? total_tiles : 0, kblocks, static_cast<int>(gridDim.x) / C::RANKS, p.max_parts,
                 static_cast<int>(blockIdx.x) / C::RANKS);
   volatile int *abort_flag = &s.abort_flag;
   int issued = 0;  // k-blocks this CTA's producer has loaded
@@ -783,7 +784,8 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
         }
       }
     }
-    if (warp == 1 && lane == 0 && leader) {
+    // (a commit covers the MMAs of the lane that makes it: the elected one's)
+    if (warp == 1 && leader && elect_one()) {
       if (kPair)
         umma_commit_pair(&s.drain, 0x1);
       else

@@ -6,6 +6,8 @@ rounding.  silu(g) up: g and up are off by 3 u each, silu magnifies g's relative
 exponential is off by its argument's rounding, at most 2 |g| u, and the approximations' 2^-21 (results of 16 bits) or
 8 u (fp32): (14 + 6 |g|) u + 2^-21 together.  The approximate reciprocal drops sigmoids below 2^-126."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -59,6 +61,20 @@ def test_pointers_refused():
     init = q8.lib().moe_q8_workspace_init
     assert init(None, 1 << 20, None) == 1 and init(ODD, 1 << 20, None) == 3 and init(A, 256, None) == 4
     assert q8.lib().moe_q8_matmul(None, A, A, A, A, A, None, A, A, 1 << 40, None) == 1
+
+
+def test_headers_are_plain_c(tmp_path):
+    src = tmp_path / "client.c"
+    src.write_text('#include "srm_rows.h"\n#include "srm_q8.h"\n'
+                   "int main(void) { moe_q8_matmul_t c = {1, 32, 16, 1, 0, MOE_DTYPE_BF16, 16, 32, 32};\n"
+                   "moe_rows_cfg_t r = {0};\n"
+                   "return (moe_q8_matmul_workspace_size(&c) > 0 && moe_rows_sort_grad(&r, 0, 0, 0, 0, 0) == MOE_ERR_ARG)"
+                   " ? 0 : 1; }\n")
+    lib_dir, exe = os.path.dirname(moe.LIB_PATH), tmp_path / "client"
+    inc = os.path.join(os.path.dirname(lib_dir), "include")
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", inc, str(src), "-L", lib_dir, "-lsrm_moe",
+                    "-Wl,-rpath," + lib_dir, "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
 
 
 # ------------------------------------------------------------------ on the GPU
