@@ -103,7 +103,7 @@ typedef struct {
 
 /* Bytes of device workspace for this shape; 0 for an invalid one.  A workspace
  * for R rows serves every product of no more rows, whatever its other sizes,
- * one call at a time (at most 39 MB on 148 SMs). */
+ * one call at a time (at most 20 MB on 148 SMs). */
 size_t moe_q8_matmul_workspace_size(const moe_q8_matmul_t *cfg);
 
 /* Sets a workspace's control words, once when it is allocated (asynchronous on

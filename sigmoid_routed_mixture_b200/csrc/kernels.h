@@ -182,17 +182,16 @@ struct Q8GemmArgs {
   int *err;
   int *ready;              // kQ8Ready while the counters below are zero between calls
   unsigned *tile_counter;
-  unsigned *part_counter;  // streamed: [tiles][CTAs of a unit][epilogue warps]
-  int32_t *partial;        // streamed: [units][2][CTAs of a unit][token column][128]
+  unsigned *part_counter;  // cut tiles: [tiles][CTAs of a unit][epilogue warps]
+  int32_t *partial;        // cut tiles: [units][CTAs of a unit][token column][128]
   int R, N, K, groups;
-  int streamed;            // the tiles' k-blocks in equal shares (few tiles), or whole tiles
   int units;               // CTAs (or pairs) that the work is for
-  int max_parts;           // streamed: parts a tile may be cut into
+  int max_parts;           // parts a tile may be cut into (0: tiles are dealt out whole)
   int max_mtiles;          // token blocks the workspace is laid out for
   int stall;               // failure-detection tests only: the producer issues no loads
 };
 struct Q8Plan {
-  bool pair, streamed;
+  bool pair;
   int units, max_parts;
   int64_t max_mtiles;
 };

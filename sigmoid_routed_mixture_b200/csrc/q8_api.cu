@@ -92,9 +92,9 @@ moe_status_t check_matmul(const moe_q8_matmul_t *c) {
 // serves products of several shapes in turn.
 constexpr size_t kReadyOffset = 128, kPartCounters = 256;
 size_t control_bytes() {
-  // streamed work has fewer than two tiles per unit (a CTA, or a pair), and a
-  // counter for each epilogue warp of a tile
-  return kPartCounters + sizeof(unsigned) * 2 * srm::kQ8EpiWarps * static_cast<size_t>((num_sms() + 31) / 32 * 32);
+  // cut tiles are no more than the units (a CTA, or two), with a counter for
+  // each epilogue warp of each CTA of a tile
+  return kPartCounters + sizeof(unsigned) * srm::kQ8EpiWarps * static_cast<size_t>((num_sms() + 31) / 32 * 32);
 }
 size_t matmul_ws_bytes(int64_t R) {
   return control_bytes() + sizeof(int32_t) * static_cast<size_t>(srm::q8_partials(R, num_sms()));
@@ -164,7 +164,6 @@ moe_status_t moe_q8_matmul(const moe_q8_matmul_t *cfg, const int8_t *x, const fl
   p.N = cfg->N;
   p.K = cfg->K;
   p.groups = cfg->groups;
-  p.streamed = plan.streamed;
   p.units = plan.units;
   p.max_parts = plan.max_parts;
   p.max_mtiles = static_cast<int>(plan.max_mtiles);

@@ -14,14 +14,12 @@
 // token block fastest.  A k-block moves the bytes of a 16-bit one in the same
 // MMA time and covers twice the K.
 //
-// Streamed reduction: with few tiles the tiles' k-blocks, laid end to end, are
-// dealt to the CTAs (or pairs) in equal contiguous shares, so that all of them
-// read weights until the end whatever the tile count.  A share starts and ends
-// inside tiles: for such a part the epilogue warps leave their int32 partial
-// sums in the workspace and count themselves in, and the last of a tile's
-// parts to arrive adds the others' sums to its own accumulator and finishes.
-// Nothing waits, and integer sums are exact in any order, so the result does
-// not change from run to run.
+// Split reduction: where there are fewer tiles than CTAs (or pairs), each
+// tile's K range is cut into equal parts, one a unit.  The epilogue warps of a
+// part leave their int32 partial sums in the workspace and count themselves
+// in, and the last of a tile's parts to arrive adds the others' sums to its own
+// accumulator and finishes.  Nothing waits, and integer sums are exact in any
+// order, so the result does not change from run to run.
 //
 // The counters return to zero by themselves (each wraps at its last arrival),
 // so a call needs no clearing launch before it (1 to 3 us of a decode
@@ -145,8 +143,7 @@ struct Tile {
   int rows;      // valid token rows
   int n;         // MMA N: rows rounded up to 32
   int w0;        // first weight row within the group
-  int id;        // tile number
-  int kb0, kb1;  // k-blocks of it to do here (all of them unless streamed)
+  int kb0, kb1;  // k-blocks of it to do here (all of them unless it is cut)
 };
 
 // Tiles in (group, weight block, token block) order, token block fastest
@@ -156,10 +153,9 @@ template <bool kPair>
 __device__ __forceinline__ Tile decode(const Smem &s, const Q8GemmArgs &p, int n_tiles, int m_chunk,
                                        int kblocks, int tile) {
   Tile c;
-  c.id = tile;
   c.kb0 = 0;
   c.kb1 = kblocks;
-  const int mt_flat = c.id / n_tiles;
+  const int mt_flat = tile / n_tiles;
   int lo = 0, hi = p.groups - 1;  // last g with tile_start[g] <= mt_flat
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -169,7 +165,7 @@ __device__ __forceinline__ Tile decode(const Smem &s, const Q8GemmArgs &p, int n
       hi = mid - 1;
   }
   const int mblocks = s.tile_start[lo + 1] - s.tile_start[lo];
-  const int local = c.id - s.tile_start[lo] * n_tiles;
+  const int local = tile - s.tile_start[lo] * n_tiles;
   // (a group of at most m_chunk token blocks, the usual one, needs no division)
   const int m0 = mblocks <= m_chunk ? 0 : local / n_tiles / m_chunk * m_chunk;
   const int cm = min(m_chunk, mblocks - m0);  // token blocks in this chunk
@@ -193,47 +189,10 @@ __device__ __forceinline__ bool ring_tile(const Smem &s, uint32_t ts, int kblock
   c->rows = e[2];
   c->w0 = e[3];
   c->n = max(32, (c->rows + 31) & ~31);
-  c->id = 0;  // only parts of streamed tiles are counted
   c->kb0 = 0;
   c->kb1 = kblocks;
   return c->g >= 0;
 }
-
-// A unit's share of the streamed k-blocks: [begin(u), begin(u + 1)) of
-// tiles * kblocks, walked part by part (a part lies in one tile).
-struct Stream {
-  int64_t total, pos, end;
-  int units, kblocks;
-  // With no more tiles than units, every tile in equal parts: the number of
-  // tiles is only known here, a group's rows being the device's to know.
-  // Otherwise the shares straddle tiles.  No share is empty either way.
-  __device__ __forceinline__ Stream(int64_t tiles, int kblocks_, int units_, int max_parts, int unit)
-      : total(tiles * kblocks_), pos(0), end(0), units(units_), kblocks(kblocks_) {
-    if (tiles == 0) return;
-    if (tiles <= units)
-      units = static_cast<int>(tiles * min(min(max_parts, kblocks), units / static_cast<int>(tiles)));
-    if (unit < units) {
-      pos = begin(unit);
-      end = begin(unit + 1);
-    }
-  }
-  __device__ __forceinline__ int64_t begin(int unit) const { return unit * total / units; }
-  // the unit whose share holds k-block q: the last u with u * total / units <= q
-  __device__ __forceinline__ int unit_of(int64_t q) const {
-    return static_cast<int>(((q + 1) * units - 1) / total);
-  }
-  template <bool kPair>
-  __device__ __forceinline__ bool next(const Smem &s, const Q8GemmArgs &p, int n_tiles, int m_chunk, Tile *c) {
-    if (pos >= end) return false;
-    const int tile = static_cast<int>(pos / kblocks);
-    *c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, tile);
-    c->kb0 = static_cast<int>(pos - static_cast<int64_t>(tile) * kblocks);
-    const int64_t left = end - pos;
-    if (left < kblocks - c->kb0) c->kb1 = c->kb0 + static_cast<int>(left);
-    pos += c->kb1 - c->kb0;
-    return true;
-  }
-};
 
 // Two results (of two rows) in their type.  fp16 saturates at +-65504, as the
 // library's other fp16 intermediates do: an infinity becomes the largest finite
@@ -400,9 +359,20 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
   const uint32_t tmem_base = s.tmem_base;
   const int total_tiles = s.total_mtiles * n_tiles;
   const bool counted = s.ready != 0;
-  const bool streamed = p.streamed && counted;
-  Stream stream(streamed ? total_tiles : 0, kblocks, static_cast<int>(gridDim.x) / C::RANKS, p.max_parts,
-                static_cast<int>(blockIdx.x) / C::RANKS);
+  const int units = static_cast<int>(gridDim.x) / C::RANKS;
+  const int unit = static_cast<int>(blockIdx.x) / C::RANKS;
+  // Cut tiles: unit u has part u % parts of tile u / parts.  The number of
+  // tiles is only known here, a group's rows being the device's to know.
+  const bool cut = p.max_parts > 0 && counted && total_tiles > 0 && total_tiles <= units;
+  const int parts = cut ? min(min(p.max_parts, kblocks), units / total_tiles) : 1;
+  const int my_tile = unit / parts, my_part = unit - my_tile * parts;
+  auto cut_tile = [&](Tile *c) {
+    if (my_tile >= total_tiles) return false;
+    *c = decode<kPair>(s, p, n_tiles, m_chunk, kblocks, my_tile);
+    c->kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * my_part / parts);
+    c->kb1 = static_cast<int>(static_cast<int64_t>(kblocks) * (my_part + 1) / parts);
+    return true;
+  };
   volatile int *abort_flag = &s.abort_flag;
   int issued = 0;  // k-blocks this CTA's producer has loaded
 
@@ -420,14 +390,13 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
     const uint32_t full0 = kPair ? cluster_map(&s.full[0], 0) : smem_addr(&s.full[0]);
     uint32_t stage = 0, phase = 0, ts = 0, tph = 0;
     uint32_t ps = 0, pph = 0;  // next ring slot to publish and its phase
-    const int stride = static_cast<int>(gridDim.x) / C::RANKS;
-    int last = static_cast<int>(blockIdx.x) / C::RANKS;  // the newest tile of this unit
+    int last = unit;  // the newest tile of this unit
     auto publish = [&](bool draw) {
       if (!mbar_wait(&s.tile_empty[ps], pph ^ 1u, abort_flag, p.err)) return false;
       if (lane == 0) {
         int t = last;
         if (draw)  // as many draws as tiles: the last one leaves the counter at 0
-          t = counted ? static_cast<int>(atomicInc(p.tile_counter, total_tiles - 1)) + stride : last + stride;
+          t = (counted ? static_cast<int>(atomicInc(p.tile_counter, total_tiles - 1)) : last) + units;
         last = t;
         // the other roles (and the peer) get the tile's place worked out
         Tile c;
@@ -452,11 +421,11 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
       }
       return true;
     };
-    bool ok = streamed || !leader || publish(false);
-    while (ok && !p.stall) {
+    bool ok = cut || !leader || publish(false);
+    for (bool first = true; ok && !p.stall; first = false) {
       Tile c;
-      if (streamed) {
-        if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
+      if (cut) {
+        if (!first || !cut_tile(&c)) break;
       } else {
         if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
         const bool any_left = ring_tile(s, ts, kblocks, &c);
@@ -476,7 +445,7 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
       const uint32_t tx = (kPair ? 2u : 1u) * static_cast<uint32_t>(A_BYTES + (32 << box) * BK);
       const int draw_at = max(c.kb0, c.kb1 - STAGES);
       for (int kb = c.kb0; kb < c.kb1; ++kb) {
-        if (leader && !streamed && kb == draw_at && !publish(true)) {
+        if (leader && !cut && kb == draw_at && !publish(true)) {
           ok = false;
           break;
         }
@@ -504,10 +473,10 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
       const uint64_t a_desc0 = umma_desc_sw128(smem_addr(sA)), b_desc0 = umma_desc_sw128(smem_addr(sB));
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, ts = 0, tph = 0;
       int consumed = 0;
-      while (true) {
+      for (bool first = true;; first = false) {
         Tile c;
-        if (streamed) {
-          if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
+        if (cut) {
+          if (!first || !cut_tile(&c)) break;
         } else {
           if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err)) break;
           const bool any_left = ring_tile(s, ts, kblocks, &c);
@@ -574,11 +543,11 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
     const int m_first = (warp - 2) / 4;
     uint32_t acc = 0, acc_phase = 0, ts = 0, tph = 0;
     float *row_scale = s.row_scale[warp - 2];
-    while (true) {
+    for (bool first = true;; first = false) {
       Tile c;
       const uint32_t slot = ts;
-      if (streamed) {
-        if (!stream.next<kPair>(s, p, n_tiles, m_chunk, &c)) break;
+      if (cut) {
+        if (!first || !cut_tile(&c)) break;
       } else {
         if (!mbar_wait(&s.tile_full[ts], tph, abort_flag, p.err, kPair)) break;
         const bool any_left = ring_tile(s, ts, kblocks, &c);
@@ -618,20 +587,14 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
       if (!mbar_wait(&s.tfull[acc], acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + acc * BT + (static_cast<uint32_t>(q * 32) << 16);
-      const bool part = c.kb1 - c.kb0 < kblocks;
       bool mine = any;
-      // a part's sums: [unit][its first or another part][CTA][column][lane]
+      // a part's sums: [unit][CTA][column][lane]
       constexpr int64_t SLAB = static_cast<int64_t>(BT) * BM;
-      const int unit = static_cast<int>(blockIdx.x) / C::RANKS;
-      const int64_t tile0 = static_cast<int64_t>(c.id) * kblocks;
-      int first_unit = unit, last_unit = unit;
       auto slab = [&](int u) {
-        const int later = stream.begin(u) < tile0 ? 1 : 0;  // the unit starts in an earlier tile
-        return p.partial + ((static_cast<int64_t>(u) * 2 + later) * C::RANKS + rank) * SLAB + q * 32 + lane;
+        return p.partial + (static_cast<int64_t>(u) * C::RANKS + rank) * SLAB + q * 32 + lane;
       };
-      if (part && any) {
-        first_unit = stream.unit_of(tile0);
-        last_unit = stream.unit_of(tile0 + kblocks - 1);
+      const int first_unit = unit - my_part;
+      if (parts > 1 && any) {
         int32_t *dst = slab(unit);
         for (int m = m_first; 32 * m < c.n; m += STEP) {
           uint32_t cv[32];
@@ -645,8 +608,8 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
         int seen = 0;
         if (lane == 0)
           seen = static_cast<int>(
-              atomicInc(p.part_counter + (c.id * C::RANKS + rank) * EPI_WARPS + warp - 2, last_unit - first_unit));
-        mine = __shfl_sync(0xffffffffu, seen, 0) == last_unit - first_unit;
+              atomicInc(p.part_counter + (my_tile * C::RANKS + rank) * EPI_WARPS + warp - 2, parts - 1));
+        mine = __shfl_sync(0xffffffffu, seen, 0) == parts - 1;
         __threadfence();
       }
       uint32_t largest = 0;
@@ -661,7 +624,7 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
           uint32_t cv[32];
           tmem_ld32(taddr + 32 * m, cv);
           tmem_ld_wait();
-          for (int u = first_unit; u <= last_unit; ++u) {
+          for (int u = first_unit; u < first_unit + parts; ++u) {
             if (u == unit) continue;
             const int32_t *src = slab(u) + 32 * m * BM;
 #pragma unroll
@@ -752,10 +715,10 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
       if (lane == 0) {
         if (leader) {
           mbar_arrive(&s.tempty[acc]);
-          if (!streamed) mbar_arrive(&s.tile_empty[slot]);
+          if (!cut) mbar_arrive(&s.tile_empty[slot]);
         } else {
           mbar_arrive_remote(cluster_map(&s.tempty[acc], 0));
-          if (!streamed) mbar_arrive_remote(cluster_map(&s.tile_empty[slot], 0));
+          if (!cut) mbar_arrive_remote(cluster_map(&s.tile_empty[slot], 0));
         }
       }
       acc ^= 1u;
@@ -884,18 +847,20 @@ cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const Q8Maps &tmap
 
 // The tile shape, and how the work is dealt out.
 //   CTA pairs or single CTAs: a k-block takes about the same time in either
-//   (0.27 and 0.29 us) and a pair's covers four times the products per CTA,
-//   but a single CTA's tile starts and ends sooner.  Single ones while a group
-//   holds at most 64 rows (64 x 24576 x 6144: 38 us against 42), and while all
-//   their tiles run at once (777 x 1001 x 2064: 14 against 19 us); pairs above
-//   (256 x 6144 x 12288: 40 against 53).
-//   Streamed with no more tiles than units: each tile is cut into equal parts,
-//   so many that a further one would cost more (about 2 us of exchange for
-//   single CTAs, 6 for pairs) than its share of the tile's k-blocks.  Single
-//   CTAs also up to twice as many tiles, their shares then straddling tiles
-//   (1 x 24576 x 6144, 192 tiles: 33 us against 38 dealt out whole); for pairs
-//   the exchange costs more than the uneven end (4096 x 2048 x 1536, 128 tiles:
-//   40 us against 19).
+//   and a pair's covers four times the products per CTA, but a single CTA's
+//   tile starts and ends sooner.  Single ones while a group holds at most 64
+//   rows (64 x 24576 x 6144: 31.6 us against 33.7; 512 tokens on 64 experts of
+//   2048 x 1536: 40.5 against 44.0), and while all their tiles run at once (777 x
+//   1001 x 2064: 9.9 against 14.2 us); pairs above (256 x 6144 x 12288: 32 against
+//   40; 1024 tokens on the 64 experts: 47.6 against 48.0).
+//   Tiles that are no more than the units are cut into parts where that pays.
+//   In k-blocks' time, cutting a tile of kb k-blocks in p parts costs 10 + 4 p
+//   for single CTAs and 21 p - 10 for pairs, whose partial sums are four times
+//   as large (measured at kb = 16 to 512: 1 x 128 x 65536 whole 92 us, in 4 parts
+//   29, in 12 19; 16 x 2048 x 2048 whole 7.3, in 2 parts 8.1; 256 x 6144 x 12288
+//   on pairs whole 36.3, in 2 parts 32.0, in 3 33.2).  Shares that straddle tiles,
+//   to even out a number of tiles just above the units, cost more than they
+//   gave (1 x 24576 x 6144, 192 tiles: 31.8 us against 29.9 dealt out whole).
 Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms) {
   Q8Plan p;
   const int64_t touched = R < groups ? R : groups;
@@ -906,22 +871,23 @@ Q8Plan q8_plan(int64_t R, int N, int K, int groups, int num_sms) {
   const int units = p.pair ? num_sms / 2 : num_sms;
   p.max_mtiles = blocks(bt);
   const int64_t tiles = p.max_mtiles * ((N + wb - 1) / wb);
-  const int64_t kblocks = (K + 127) / 128;
-  p.streamed = tiles <= units || (!p.pair && tiles < 2 * units);
   p.units = tiles < units ? static_cast<int>(tiles) : units;
-  const int64_t cost = p.pair ? 21 : 7;  // k-blocks' time that a further part costs
-  p.max_parts = 1;
-  while ((p.max_parts + 1) * p.max_parts * cost <= kblocks) ++p.max_parts;
-  if (tiles > 0 && tiles <= units)
+  p.max_parts = 0;
+  if (tiles > 0 && tiles <= units) {
+    const int kb = (K + 127) / 128;
+    auto cost = [&](int parts) { return kb / static_cast<double>(parts) + (p.pair ? 21 * parts - 10 : 10 + 4 * parts); };
+    p.max_parts = 2;
+    while (p.max_parts < kb && cost(p.max_parts + 1) < cost(p.max_parts)) ++p.max_parts;
+    if (cost(p.max_parts) >= kb) p.max_parts = 1;
     p.units = static_cast<int>(tiles * (p.max_parts * tiles <= units ? p.max_parts : units / tiles));
+  }
   return p;
 }
 
-// Two parts of a tile per unit, whatever the other sizes: a workspace for some
-// rows serves every product of no more rows.
+// One part a unit, whatever the other sizes: a workspace for some rows serves
+// every product of no more rows.
 int64_t q8_partials(int64_t R, int num_sms) {
-  return R <= kQ8SoloRows ? int64_t(num_sms) * 2 * kQ8SoloRows * 128
-                          : int64_t(num_sms / 2) * 2 * 2 * kQ8PairRows * 128;
+  return R <= kQ8SoloRows ? int64_t(num_sms) * kQ8SoloRows * 128 : int64_t(num_sms / 2) * 2 * kQ8PairRows * 128;
 }
 
 }  // namespace srm
