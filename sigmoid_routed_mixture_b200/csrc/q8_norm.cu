@@ -48,11 +48,16 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *buf) {
   return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < n ? buf[threadIdx.x & 31] : 0u);
 }
 
-// scale and the factor that takes n to q: q = rne((n * up) * r).  `up` keeps
-// 127 / max finite for rows below 2^-100.  r = 0 for a zero row; a row with an
-// infinity or NaN gets scale NaN and is written as zeros.
+// scale and the factor 127 / max that takes n to q, as the sum of two fp32
+// numbers, for rows multiplied by `up`: 1, or the power of two that brings rows
+// below 2^-100 or above 2^100 away from the ends of fp32's range.  Both are 0
+// for a zero row; a row with an infinity or NaN gets scale NaN and zeros.
+struct QFactor {
+  float hi, lo;
+};
 struct QScale {
-  float scale, up, r;
+  float scale, up;
+  QFactor r;
   bool finite;
 };
 __device__ __forceinline__ QScale q_scale(uint32_t max_bits) {
@@ -60,31 +65,62 @@ __device__ __forceinline__ QScale q_scale(uint32_t max_bits) {
   s.finite = max_bits < 0x7f800000u;
   const float m = __uint_as_float(max_bits);
   s.scale = s.finite ? m / 127.f : __uint_as_float(0x7fc00000u);
-  s.up = m < 0x1p-100f ? 0x1p100f : 1.f;
-  s.r = m > 0.f ? 127.f / (m * s.up) : 0.f;
+  s.up = m < 0x1p-100f ? 0x1p100f : m > 0x1p100f ? 0x1p-100f : 1.f;
+  s.r = {0.f, 0.f};
+  if (s.finite && m > 0.f) {
+    const float mu = m * s.up;
+    s.r.hi = 127.f / mu;
+    s.r.lo = fmaf(-s.r.hi, mu, 127.f) * (s.r.hi * (1.f / 127.f));  // a few bits of it count
+  }
   return s;
 }
 
-// Adding 1.5 * 2^23 rounds n * r to the nearest integer (ties to even) in the
-// sum's low bits, in one operation: |n * r| <= 127 (1 + 2^-22), so the low
-// byte is q in two's complement and needs no clamp.
-__device__ __forceinline__ uint32_t q_bits(float n, float r) { return __float_as_uint(fmaf(n, r, 12582912.f)); }
+// q = rne(n * 127 / max) in the low byte: n * hi + (n * lo) is within one
+// rounding of the quotient, and adding 1.5 * 2^23 rounds that to the nearest
+// integer, ties to even, in two's complement; the quotient is at most 127, so
+// nothing has to be clamped.  Without `lo` a quotient of exactly k + 1/2 went
+// to the wrong side when hi was rounded that way, one element in 70000 of fp16
+// rows.  With it such an n gives exactly k + 1/2: say hi is 127 / max (1 + d),
+// |d| <= 2^-24.  The product n * hi is then either k + 1/2, with |(k + 1/2) d|
+// at most half a unit of its last place, or the neighbour, with at least half
+// a unit; adding n * lo = -(k + 1/2) d leaves less than half a unit to
+// k + 1/2 each time.  (The last places below 1/2 are half as wide, but there
+// 1/2 and its lower neighbour both round to 0.)
+__device__ __forceinline__ uint32_t q_bits(float n, QFactor r) {
+  return __float_as_uint(fmaf(n, r.lo, n * r.hi) + 12582912.f);
+}
+__device__ __forceinline__ void q_bits2(float n0, float n1, QFactor r, uint32_t &q0, uint32_t &q1) {
+  asm("{\n\t.reg .b64 n, h, l, c;\n\t"
+      "mov.b64 n, {%2, %3};\n\t"
+      "mov.b64 h, {%4, %4};\n\t"
+      "mov.b64 l, {%5, %5};\n\t"
+      "mov.b64 c, {%6, %6};\n\t"
+      "mul.rn.f32x2 h, n, h;\n\t"
+      "fma.rn.f32x2 h, n, l, h;\n\t"
+      "add.rn.f32x2 h, h, c;\n\t"
+      "mov.b64 {%0, %1}, h;\n\t}"
+      : "=r"(q0), "=r"(q1)
+      : "f"(n0), "f"(n1), "f"(r.hi), "f"(r.lo), "f"(12582912.f));
+}
 
 __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// E consecutive q of a row that is finite and not under 2^-100 (n scaled by up).
+// E consecutive q of a row that is finite (n multiplied by up).
 template <int E>
-__device__ __forceinline__ void store_q(int8_t *p, const float (&n)[E], float r) {
+__device__ __forceinline__ void store_q(int8_t *p, const float (&n)[E], QFactor r) {
   if constexpr (E == 1) {
     *p = static_cast<int8_t>(q_bits(n[0], r));
   } else {
     uint32_t w[E / 4];
 #pragma unroll
-    for (int k = 0; k < E / 4; ++k)
-      w[k] = low_bytes(q_bits(n[4 * k], r), q_bits(n[4 * k + 1], r), q_bits(n[4 * k + 2], r),
-                       q_bits(n[4 * k + 3], r));
+    for (int k = 0; k < E / 4; ++k) {
+      uint32_t q[4];
+      q_bits2(n[4 * k], n[4 * k + 1], r, q[0], q[1]);
+      q_bits2(n[4 * k + 2], n[4 * k + 3], r, q[2], q[3]);
+      w[k] = low_bytes(q[0], q[1], q[2], q[3]);
+    }
     if constexpr (E == 8)
       *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     else
@@ -233,16 +269,15 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
 #pragma unroll
       for (int k = 0; k < E; ++k) v[j][k] = s.finite ? v[j][k] * s.up : 0.f;
   }
-  const float r = s.finite ? s.r : 0.f;
 #pragma unroll
   for (int j = 0; j < U; ++j)
-    if (there(j)) store_q<E>(q + at(j), v[j], r);
+    if (there(j)) store_q<E>(q + at(j), v[j], s.r);
 }
 
 // Quantisation alone.  Threads past the row's end take its last E elements once
 // more (the same maximum, the same bytes stored), which spares a test around
 // every step: 5003 x 1541 fp16 16 us with the tests (36 instructions an
-// element), 9 without.
+// element), 10 without (1 of them the exact ties).
 template <typename T, int E, int U, int kWarps>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     q8_quantize_kernel(const Q8RowArgs p) {
@@ -275,10 +310,19 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
 #pragma unroll
       for (int k = 0; k < E; ++k) v[j][k] = s.finite ? v[j][k] * s.up : 0.f;
   }
-  const float r = s.finite ? s.r : 0.f;
   int8_t *q = p.q + to * p.ld_q;
+  if constexpr (E == 1 && U % 2 == 0) {  // single elements: two of the row's at once
 #pragma unroll
-  for (int j = 0; j < U; ++j) store_q<E>(q + min((j * tpr + tid) * E, last), v[j], r);
+    for (int j = 0; j < U; j += 2) {
+      uint32_t q0, q1;
+      q_bits2(v[j][0], v[j + 1][0], s.r, q0, q1);
+      q[min(j * tpr + tid, last)] = static_cast<int8_t>(q0);
+      q[min((j + 1) * tpr + tid, last)] = static_cast<int8_t>(q1);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < U; ++j) store_q<E>(q + min((j * tpr + tid) * E, last), v[j], s.r);
+  }
 }
 
 // Rows too long for one CTA's registers: element loads, three passes over the

@@ -217,6 +217,31 @@ def test_special_rows(H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,most,H,power", [
+    (torch.float16, 2047, 2048, 0), (torch.float16, 2047, 2049, -10), (torch.bfloat16, 255, 256, 100),
+    (torch.bfloat16, 255, 40001, -100), (torch.float32, 2047, 2048, 115), (torch.float32, 2047, 2055, -130),
+])
+def test_ties_go_to_even(dtype, most, H, power):
+    """Rows of the integers 0 .. M (times a power of two, signs mixed) for every M: 127 n / M is exactly k + 1/2 in
+    many places, and elsewhere at least 1 / (2 M) away from it.  Equality, against integer arithmetic."""
+    M = torch.arange(1, most + 1, dtype=torch.int64, device="cuda")[:, None]
+    n = torch.minimum(torch.arange(H, dtype=torch.int64, device="cuda")[None], M)
+    q2 = 254 * n + M  # twice M times (the quotient + 1/2)
+    want = q2 // (2 * M)
+    tie = q2 % (2 * M) == 0
+    assert int(tie.sum()) > 200  # 253 for M up to 255
+    want -= (tie & (want % 2 == 1)).long()
+    sign = 1 - 2 * ((n + M) % 3 == 0).long()
+    x = (n * sign).double() * 2.0 ** power
+    assert torch.equal(x.to(dtype).double(), x)
+    q, scale = q8.quantize(x.to(dtype))
+    assert torch.equal(q.long(), want * sign)
+    q = q8.quantize(x.to(dtype)[:, : most // 2 + 1])[0]  # rows of fewer threads; M above it gives another maximum
+    cut = M[:, 0] <= most // 2
+    assert torch.equal(q.long()[cut], (want * sign)[cut, : most // 2 + 1])
+
+
+@pytest.mark.gpu
 def test_other_stream_capture_and_empty():
     x, gamma = rows(64, 512, torch.bfloat16, 10), rows(1, 512, torch.bfloat16, 11)[0]
     want = q8.add_rmsnorm(x, gamma)
