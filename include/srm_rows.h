@@ -18,7 +18,7 @@
  *                         dys[pos[T*K+t]] = dy[t],
  *                         dgate[t][k] = sum_h dy[t][h] ys[pos[t*K+k]][h]
  * (the residual's gradient is dy itself).  Products and sums are fp32, in slot
- * order with the shared row last, and rounded once: deterministic, no atomics.
+ * order with the shared row last, and rounded once: deterministic.
  *
  * An assignment without a row (pos -1: moe_permute skips expert ids out of
  * range) adds nothing, gets no gradient row and dgate 0.  Positions past
@@ -65,7 +65,8 @@ typedef struct {
  *   pos: int32 [P] out, -1 where no position holds the row
  *   xs: dtype [P][H] out;  xs_scale: fp32 [P] out (with x_scale)
  * A row id out of range, or a total outside 0..P, is ignored and flagged
- * MOE_ERR_BAD_INDEX on the device. */
+ * MOE_ERR_BAD_INDEX on the device.  So is a row id's second position: the last
+ * one takes the row, the others' rows of xs are left as they were. */
 moe_status_t moe_rows_sort(const moe_rows_cfg_t *cfg, const void *x, const float *x_scale,
                            const int32_t *offsets, const int32_t *sorted, int32_t *pos, void *xs,
                            float *xs_scale, void *ws, void *stream);
@@ -83,7 +84,8 @@ moe_status_t moe_rows_sort_grad(const moe_rows_cfg_t *cfg, const void *dxs, cons
 /*   dy: dtype [T][H];  ys: slot_dtype [P][H];  gate: fp32 [T][K] or NULL
  *   dys: slot_dtype [P][H] out, or NULL (no row gradient); may be ys itself
  *   dgate: fp32 [T][K] out, or NULL (then ys is not read and may be NULL)
- * With dys == ys each element is read before it is overwritten. */
+ * With dys == ys each element is read before it is overwritten.  pos holds no
+ * position twice, as moe_rows_sort leaves it. */
 moe_status_t moe_rows_unsort_grad(const moe_rows_cfg_t *cfg, const void *dy, const void *ys,
                                   const float *gate, const int32_t *pos, void *dys, float *dgate, void *ws,
                                   void *stream);

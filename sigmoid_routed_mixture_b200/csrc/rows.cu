@@ -3,8 +3,9 @@
 //
 // All of it is bound by memory: each token row is read once and each sorted
 // row written once, or the reverse; the gradient of the way back reads dy once
-// for all of a token's slots.  No atomics: every output element is the work of
-// one thread, and a sum over slots or over a row runs in a fixed order.
+// for all of a token's slots.  No atomics on values: every output element is
+// the work of one thread, and a sum over slots or over a row runs in a fixed
+// order.  (The inverse is a maximum of positions, whose order does not matter.)
 #include <type_traits>
 
 #include "kernels.h"
@@ -73,6 +74,13 @@ __device__ __forceinline__ int row_pos(const int32_t *pos, int a, int P, int *er
   return -1;
 }
 
+// pos[a] = p for the row id a that position p holds.  An id in two positions
+// (of a list that is no permutation) goes to the later one, whatever the order
+// of the threads, and is flagged.
+__device__ __forceinline__ void invert(int32_t *pos, int a, int p, int P, int *err) {
+  if (a < 0 || a >= P || atomicMax(&pos[a], p) >= 0) record_error(err, MOE_ERR_BAD_INDEX);
+}
+
 constexpr int kBatch = 8;              // vectors a lane has in flight
 constexpr int kSmallPositions = 4096;  // the inverse in every CTA's shared memory: 16 KB
 
@@ -84,13 +92,7 @@ __global__ void __launch_bounds__(256)
                        const int32_t *__restrict__ sorted, int32_t *__restrict__ pos) {
   previous_done();
   const int n = row_total(offsets, p.E + 1, p.P, p.err);
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-    const int a = sorted[i];
-    if (a < 0 || a >= p.P)
-      record_error(p.err, MOE_ERR_BAD_INDEX);
-    else
-      pos[a] = i;
-  }
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) invert(pos, sorted[i], i, p.P, p.err);
 }
 
 // The rows by token: each token row is read once and written to its positions
@@ -171,12 +173,16 @@ __global__ void __launch_bounds__(256)
   __syncthreads();
   previous_done();
   const int n = row_total(offsets, p.E + 1, p.P, p.err);
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int a = sorted[i];
-    if (a < 0 || a >= p.P)
-      record_error(p.err, MOE_ERR_BAD_INDEX);
-    else
-      inverse[a] = i;
+  // four ids on their way at a time (64 tokens x 9 rows of 12 KB, 400 of 4 KB: 4.0
+  // and 6.6 us, with one 4.5 and 8.1, with eight 4.1 and 6.3)
+  for (int i = threadIdx.x; i < n; i += 1024) {
+    int a[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + 256 * j < n) a[j] = sorted[i + 256 * j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + 256 * j < n) invert(inverse, a[j], i + 256 * j, p.P, p.err);
   }
   __syncthreads();
   if (blockIdx.x == 0)

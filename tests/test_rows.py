@@ -289,6 +289,30 @@ def test_bad_ids_and_positions_are_flagged(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [20, 2000])  # the inverse in one launch, and in several
+def test_id_in_two_positions(T):
+    """The later position takes the row, in every run; the other's row of xs stays as it was."""
+    H, E, K = 32, 4, 2
+    cfg = rows.Config(T, H, E, K)
+    gate, offsets, ids, pos = routing(T, E, K, True, 14)
+    x = torch.randn(T, H, generator=gen(15), device="cuda").to(torch.bfloat16)
+    twice = ids.clone()
+    P = cfg.rows
+    twice[1::3] = ids[0:P - 1:3][:len(twice[1::3])]  # each third id in the next position too
+    last = torch.full((P,), -1, dtype=torch.int64, device="cuda")
+    last.scatter_reduce_(0, twice.long(), torch.arange(P, device="cuda"), "amax")
+    ws = rows.workspace()
+    for _ in range(3):
+        out = torch.full((P, H), 3.0, dtype=torch.bfloat16, device="cuda")
+        xs, p = rows.sort(cfg, x, offsets, twice, ws, out=out)
+        assert torch.equal(p.long(), last) and moe.device_error(ws) == 5
+        want = torch.full_like(out, 3.0)
+        held = last[last >= 0]
+        want[held] = x[token_of(twice, T, K)][held]
+        assert torch.equal(xs, want)
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences():
     """A scalar of the whole way (sort, a linear map per position, unsort) in fp32 rows, differenced."""
     T, H, E, K = 6, 16, 5, 2
