@@ -871,9 +871,10 @@ cudaError_t launch_q8_gemm(bool swiglu, int dtype, bool pair, const Q8Maps &tmap
 //   and a pair's covers four times the products per CTA, but a single CTA's
 //   tile starts and ends sooner.  Single ones while a group holds at most 64
 //   rows (64 x 24576 x 6144: 31.6 us against 33.7; 512 tokens on 64 experts of
-//   2048 x 1536: 40.5 against 44.0), and while all their tiles run at once (777 x
-//   1001 x 2064: 9.9 against 14.2 us); pairs above (256 x 6144 x 12288: 32 against
-//   40; 1024 tokens on the 64 experts: 47.6 against 48.0).
+//   2048 x 1536: 39.6 against 42.1), and while all their tiles run at once (160 x
+//   6144 x 12288: 23.7 against 25.8 us); pairs above (256 x 6144 x 12288: 30.3
+//   against 41; 1024 tokens on the 64 experts: 44.9 against 45.1, 1536: 47.0
+//   against 54.9).
 //   Tiles that are no more than the units are cut into parts where that pays.
 //   In k-blocks' time, cutting a tile of kb k-blocks in p parts costs 10 + 4 p
 //   for single CTAs and 21 p - 10 for pairs, whose partial sums are four times
