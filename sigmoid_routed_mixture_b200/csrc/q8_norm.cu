@@ -128,6 +128,33 @@ __device__ __forceinline__ void store_q(int8_t *p, const float (&n)[E], QFactor 
   }
 }
 
+// Elements [from, to) of the E at p: as one vector where that is all of them
+// and p is aligned, else one by one (zeros for the others).
+template <typename R, int E, typename S>
+__device__ __forceinline__ R load_part(const S *p, int from, int to) {
+  static_assert(sizeof(R) == E * sizeof(S), "a unit of E elements");
+  R r;
+  if (from <= 0 && to >= E && reinterpret_cast<uintptr_t>(p) % sizeof(R) == 0) {
+    r = *reinterpret_cast<const R *>(p);
+  } else {
+    S e[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) e[k] = k >= from && k < to ? p[k] : S{};
+    memcpy(&r, e, sizeof(R));
+  }
+  return r;
+}
+template <typename T, int E>
+__device__ __forceinline__ void store_part(T *p, const float (&f)[E], int from, int to) {
+  if (from <= 0 && to >= E) {
+    RowIo<T, E>::store(p, f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k >= from && k < to) p[k] = from_float<T>(f[k]);
+  }
+}
+
 // Where a row goes: itself, or (packing the gate and up weights) row f of W1 /
 // W3 to row (f / 16) * 32 + f % 16 (+ 16 for W3) of the interleaved matrix.
 __device__ __forceinline__ int64_t dst_row(int64_t t, int unit_offset) {
@@ -138,7 +165,7 @@ __device__ __forceinline__ int64_t dst_row(int64_t t, int unit_offset) {
 
 // kWarps == 1: a warp per row (several rows a CTA); otherwise a CTA per row.
 // All of a row's loads (x, delta, gamma) are in flight before the first use.
-// Rows that are not 16-byte aligned (E = 1) take code without a test around
+// Rows whose elements are moved singly (E = 1) take code without a test around
 // every element: threads past the row's end take its last element once more,
 // which only the sum of squares has to leave out; a barrier keeps them from
 // reading it after its owner has stored over it (4096 x 1541 bf16: 40 us with
@@ -276,7 +303,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
 
 // Quantisation alone.  Threads past the row's end take its last E elements once
 // more (the same maximum, the same bytes stored), which spares a test around
-// every step: 5003 x 1541 fp16 16 us with the tests (36 instructions an
+// every step: 5003 x 1541 fp16, singly, 16 us with the tests (36 instructions an
 // element), 10 without (1 of them the exact ties).
 template <typename T, int E, int U, int kWarps>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
@@ -325,6 +352,132 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
   }
 }
 
+// Rows that start at any element, in matrices that are aligned as a whole and
+// whose row strides leave the same remainder of E: the units are those of the
+// matrices, so a row's first and last one may be shared with its neighbours
+// (each row's thread moves its own elements of them singly) and all others are
+// whole vectors.  gamma, which starts anew in each row, is read singly except
+// where it happens to be aligned.  (4096 x 1541 bf16 with sum, norm and 8 bits:
+// 20.4 us, all elements singly 25.7; quantised alone 5003 x 1541 fp16 7.5 against
+// 9.9.)
+template <typename T, int U, int kWarps, bool kPlain>
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
+    q8_offset_rows_kernel(const Q8RowArgs p) {
+  constexpr int E = kVec<T>;
+  using Io = RowIo<T, E>;
+  using Raw = typename Io::Raw;
+  __shared__ float sum_buf[2][32];
+  __shared__ uint32_t max_buf[32];
+  const int tid = kWarps == 1 ? (threadIdx.x & 31) : threadIdx.x;
+  const int tpr = kWarps == 1 ? 32 : blockDim.x;
+  const int64_t t = kWarps == 1 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : blockIdx.x;
+  if (t >= p.T) return;  // whole warps (or CTAs) only
+  previous_done();
+  // the row is elements lo .. hi - 1 from the unit that holds its first one
+  const int lo = static_cast<int>(t * p.ld_x % E), hi = lo + p.H;
+  auto at = [&](int j) { return (j * tpr + tid) * E; };
+  const T *x = static_cast<const T *>(p.x) + (t * p.ld_x - lo);
+  Raw rx[U], rd[kPlain ? 1 : U], rg[kPlain ? 1 : U];
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    rx[j] = Raw{};
+    if (at(j) < hi) rx[j] = load_part<Raw, E>(x + at(j), lo - at(j), hi - at(j));
+  }
+  if (!kPlain && p.delta) {
+    const T *delta = static_cast<const T *>(p.delta) + (t * p.ld_delta - lo);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      rd[kPlain ? 0 : j] = Raw{};
+      if (at(j) < hi) rd[kPlain ? 0 : j] = load_part<Raw, E>(delta + at(j), lo - at(j), hi - at(j));
+    }
+  }
+  if (!kPlain && p.gamma) {
+    const T *gamma = static_cast<const T *>(p.gamma) - lo;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      rg[kPlain ? 0 : j] = Raw{};
+      if (at(j) < hi) rg[kPlain ? 0 : j] = load_part<Raw, E>(gamma + at(j), lo - at(j), hi - at(j));
+    }
+  }
+  float v[U][E];
+#pragma unroll
+  for (int j = 0; j < U; ++j) Io::unpack(rx[j], v[j]);
+  if (!kPlain && p.delta) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      float d[E];
+      Io::unpack(rd[kPlain ? 0 : j], d);
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[j][k] = to_float(from_float<T>(v[j][k] + d[k]));
+    }
+  }
+  if (!kPlain && p.x_sum) {
+    T *x_sum = static_cast<T *>(p.x_sum) + (t * p.ld_sum - lo);
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (at(j) < hi) store_part<T, E>(x_sum + at(j), v[j], lo - at(j), hi - at(j));
+  }
+  if (!kPlain && p.gamma) {
+    float ss = 0.f;  // the elements outside the row are zeros
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int k = 0; k < E; ++k) ss = fmaf(v[j][k], v[j][k], ss);
+    float ms = row_sum<kWarps>(ss, sum_buf[0]) / static_cast<float>(p.H) + p.eps;
+    if (!(ms >= 0x1p-100f && ms <= 0x1p120f)) {  // as in q8_rows_kernel
+      const float f = ms < 0x1p-100f ? 0x1p96f : 0x1p-96f;
+      ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          v[j][k] *= f;
+          ss = fmaf(v[j][k], v[j][k], ss);
+        }
+      ms = row_sum<kWarps>(ss, sum_buf[1]) / static_cast<float>(p.H) + (p.eps * f) * f;
+    }
+    const float inv = 1.0f / sqrtf(ms);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      float g[E];
+      Io::unpack(rg[kPlain ? 0 : j], g);
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[j][k] = v[j][k] * inv * g[k];
+    }
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < U; ++j)
+#pragma unroll
+    for (int k = 0; k < E; ++k) m = max(m, abs_bits(v[j][k]));
+  if (!kPlain && p.y) {
+    T *y = static_cast<T *>(p.y) + (t * p.ld_y - lo);
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (at(j) < hi) store_part<T, E>(y + at(j), v[j], lo - at(j), hi - at(j));
+  }
+  const QScale s = q_scale(row_max<kWarps>(m, max_buf));
+  if (tid == 0) p.scale[t] = s.scale;
+  if (!s.finite || s.up != 1.f) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[j][k] = s.finite ? v[j][k] * s.up : 0.f;
+  }
+  int8_t *q = p.q + (t * p.ld_q - lo);
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int from = lo - at(j), to = hi - at(j);
+    if (from <= 0 && to >= E) {
+      store_q<E>(q + at(j), v[j], s.r);
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k)
+        if (k >= from && k < to) q[at(j) + k] = static_cast<int8_t>(q_bits(v[j][k], s.r));
+    }
+  }
+}
+
 // Rows too long for one CTA's registers: element loads, three passes over the
 // row.  x_sum and y are written in the last pass only, each element by the
 // thread that has just read it, so that they may be x or delta themselves.
@@ -369,8 +522,10 @@ __global__ void __launch_bounds__(1024) q8_long_rows_kernel(const Q8RowArgs p) {
 }
 
 // y = q * scale.  tpr threads (a power of two) share a row, each with kBatch
-// loads of E elements in flight; 256 / tpr rows a CTA.
-template <typename T, int E>
+// loads of E elements in flight; 256 / tpr rows a CTA.  kOffset: rows that
+// start at any element, as in q8_offset_rows_kernel (5003 x 1541 to fp16: 4.8 us,
+// all elements singly 8.5).
+template <typename T, int E, bool kOffset>
 __global__ void __launch_bounds__(256)
     q8_dequantize_kernel(const int8_t *q, const float *scale, T *y, int64_t T_, int H, int64_t ld_q,
                          int64_t ld_y, int tpr_log2) {
@@ -381,17 +536,25 @@ __global__ void __launch_bounds__(256)
   const int64_t t = (static_cast<int64_t>(blockIdx.x) << (8 - tpr_log2)) + (threadIdx.x >> tpr_log2);
   if (t >= T_) return;
   previous_done();
-  const int8_t *src = q + t * ld_q;
-  T *dst = y + t * ld_y;
+  const int lo = kOffset ? static_cast<int>(t * ld_q % E) : 0;
+  const int hi = kOffset ? lo + H : H;
+  const int8_t *src = q + t * ld_q - lo;
+  T *dst = y + t * ld_y - lo;
   const float s = scale[t];
-  for (int i0 = tid * E; i0 < H; i0 += kBatch * tpr * E) {
+  for (int i0 = tid * E; i0 < hi; i0 += kBatch * tpr * E) {
     Word w[kBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      if (i0 + j * tpr * E < H) w[j] = *reinterpret_cast<const Word *>(src + i0 + j * tpr * E);
+    for (int j = 0; j < kBatch; ++j) {
+      if constexpr (kOffset) {
+        const int c = i0 + j * tpr * E;
+        if (c < hi) w[j] = load_part<Word, E>(src + c, lo - c, hi - c);
+      } else {
+        if (i0 + j * tpr * E < H) w[j] = *reinterpret_cast<const Word *>(src + i0 + j * tpr * E);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      if (i0 + j * tpr * E >= H) break;
+      if (i0 + j * tpr * E >= hi) break;
       float f[E];
       if constexpr (E == 1) {
         f[0] = w[j] * s;
@@ -407,7 +570,12 @@ __global__ void __launch_bounds__(256)
         for (int k = 0; k < E; ++k)
           f[k] = static_cast<float>(static_cast<int8_t>(u[k / 4] >> (8 * (k % 4)))) * s;
       }
-      RowIo<T, E>::store(dst + i0 + j * tpr * E, f);
+      if constexpr (kOffset) {
+        const int c = i0 + j * tpr * E;
+        store_part<T, E>(dst + c, f, lo - c, hi - c);
+      } else {
+        RowIo<T, E>::store(dst + i0 + j * tpr * E, f);
+      }
     }
   }
 }
@@ -446,6 +614,22 @@ cudaError_t launch_rows_e(const Q8RowArgs &p, int num_sms, cudaStream_t stream) 
   return launch_overlapped(q8_long_rows_kernel<T>, static_cast<unsigned>(p.T), 1024, 0, stream, p);
 }
 
+// (512 threads at most: with more the norm spills its registers)
+template <typename T, int U>
+cudaError_t launch_rows_offset(const Q8RowArgs &p, int units, cudaStream_t stream) {
+  const int threads = ((units + U - 1) / U + 31) & ~31;
+  const unsigned rows = static_cast<unsigned>(p.T);
+  const bool plain = is_plain(p);
+  auto go = [&](auto full, auto quantize) {
+    auto kern = plain ? quantize : full;
+    return threads <= 32 ? launch_overlapped(kern, (rows + 3) / 4, 128, 0, stream, p)
+                         : launch_overlapped(kern, rows, threads, 0, stream, p);
+  };
+  if (threads <= 32) return go(q8_offset_rows_kernel<T, U, 1, false>, q8_offset_rows_kernel<T, U, 1, true>);
+  if (threads <= 256) return go(q8_offset_rows_kernel<T, U, 8, false>, q8_offset_rows_kernel<T, U, 8, true>);
+  return go(q8_offset_rows_kernel<T, U, 16, false>, q8_offset_rows_kernel<T, U, 16, true>);
+}
+
 template <typename T>
 cudaError_t launch_rows_t(const Q8RowArgs &p, int num_sms, cudaStream_t stream) {
   constexpr int E = kVec<T>;
@@ -457,6 +641,20 @@ cudaError_t launch_rows_t(const Q8RowArgs &p, int num_sms, cudaStream_t stream) 
       vec(p.gamma, 0, S, 16) && vec(p.x_sum, p.ld_sum, S, 16) && vec(p.y, p.ld_y, S, 16) &&
       vec(p.q, p.ld_q, 1, E))
     return launch_rows_e<T, E>(p, num_sms, stream);
+  auto whole = [&](const void *ptr, int64_t ld, int64_t bytes) {
+    return !ptr || (reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && (p.T == 1 || ld % E == p.ld_x % E));
+  };
+  // Short rows, and middling ones that are few, are faster singly: their first
+  // and last units take two steps (bf16 norm, us with / without this: 16384 x
+  // 385 28.8 / 24.5, 16384 x 513 30.2 / 47.4, 1024 x 1001 5.0 / 4.3, 1024 x 1281
+  // 5.4 / 6.3, 4096 x 9311 91 / 224).
+  const bool gains = p.H > 1024 || (p.H > 512 && p.T > 8 * num_sms);
+  const int units = (p.H + 2 * (E - 1)) / E;  // at most, wherever a row starts
+  if (gains && p.unit_offset < 0 && whole(p.x, p.ld_x, 16) && whole(p.delta, p.ld_delta, 16) && whole(p.x_sum, p.ld_sum, 16) &&
+      whole(p.y, p.ld_y, 16) && whole(p.q, p.ld_q, E)) {
+    if (units <= 512 && p.T <= 2 * num_sms) return launch_rows_offset<T, 1>(p, units, stream);
+    if (units <= 512 * 4) return launch_rows_offset<T, 4>(p, units, stream);
+  }
   return launch_rows_e<T, 1>(p, num_sms, stream);
 }
 
@@ -464,14 +662,20 @@ template <typename T>
 cudaError_t launch_dequant_t(const int8_t *q, const float *scale, void *y, int64_t T_, int H,
                              int64_t ld_q, int64_t ld_y, cudaStream_t stream) {
   constexpr int E = kVec<T>;
-  const bool vec = H % E == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0 && ld_y % E == 0 &&
-                   reinterpret_cast<uintptr_t>(q) % E == 0 && ld_q % E == 0;
-  const int loads = vec ? H / E : H;
+  const bool whole = reinterpret_cast<uintptr_t>(y) % 16 == 0 && reinterpret_cast<uintptr_t>(q) % E == 0;
+  const bool vec = whole && H % E == 0 && ld_y % E == 0 && ld_q % E == 0;
+  // (as for the rows to 8 bits: bf16, us with / without: 1024 x 1001 2.2 / 1.9,
+  // 1024 x 1281 2.1 / 2.6, 16384 x 129 3.4 / 4.6, 1 x 6145 1.6 / 2.8)
+  const bool gains = H > 2048 || T_ * H > 5 << 18;
+  const bool offset = gains && whole && !vec && (T_ == 1 || ld_y % E == ld_q % E);
+  const int loads = vec ? H / E : offset ? (H + 2 * (E - 1)) / E : H;
   int log2 = 0;  // threads per row: four loads each
   while (log2 < 8 && (4 << log2) < loads) ++log2;
   const unsigned blocks = static_cast<unsigned>((T_ + (256 >> log2) - 1) >> (8 - log2));
-  return launch_overlapped(vec ? q8_dequantize_kernel<T, E> : q8_dequantize_kernel<T, 1>, blocks, 256, 0, stream, q,
-                           scale, static_cast<T *>(y), T_, H, ld_q, ld_y, log2);
+  auto kern = vec      ? q8_dequantize_kernel<T, E, false>
+              : offset ? q8_dequantize_kernel<T, E, true>
+                       : q8_dequantize_kernel<T, 1, false>;
+  return launch_overlapped(kern, blocks, 256, 0, stream, q, scale, static_cast<T *>(y), T_, H, ld_q, ld_y, log2);
 }
 
 }  // namespace

@@ -184,6 +184,37 @@ def test_strides_and_in_place(dtype, ld, offset):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,H,ld", [(37, 61, 67), (300, 1541, 1541), (2000, 513, 515), (9, 3, 5), (11, 1, 3), (4, 4099, 4109),
+                                    (700, 4099, 4099), (3, 16000, 16007), (6000, 257, 257)])
+def test_rows_at_any_element(T, H, ld, dtype):
+    """Aligned buffers whose rows start at any element, results in place: nothing beside the rows is touched."""
+    def buffer(seed, kind):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        return torch.randn(T * ld, generator=g, device="cuda").to(kind).view(T, ld)
+
+    xb, db, qb = buffer(20, dtype), buffer(21, dtype), torch.full((T, ld), 99, dtype=torch.int8, device="cuda")
+    x, delta, q8b = xb[:, :H], db[:, :H], qb[:, :H]
+    beside = [b[:, H:].clone() for b in (xb, db, qb)]
+    gamma = (1 + 0.1 * rows(1, H, torch.float32, 22)[0]).to(dtype)
+    sc = torch.empty(T, dtype=torch.float32, device="cuda")
+    total, n = reference(x, gamma, 1e-5, delta)
+    q, scale = q8.add_rmsnorm(x, gamma, 1e-5, delta=delta, x_out=x, y=delta, out=(q8b, sc))
+    assert torch.equal(x, total)
+    check(x, n, q, scale, delta)
+    assert all(torch.equal(b[:, H:], w) for b, w in zip((xb, db, qb), beside))
+    q, scale = q8.quantize(x, out=(q8b, sc))
+    check(x, x.double(), q, scale, normed=False)
+    want = q8.dequantize(q.contiguous(), scale, dtype)
+    assert torch.equal(q8.dequantize(q, scale, dtype, out=x), want)
+    exact = q.double() * scale.double()[:, None]
+    assert torch.all((x.double() - exact).abs() <= (torch.finfo(dtype).eps / 2 + 2 * U) * exact.abs() +
+                     torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps)
+    assert all(torch.equal(b[:, H:], w) for b, w in zip((xb, db, qb), beside))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("H", [64, 37, 2048, 40001])
 def test_special_rows(H):
     dt = torch.float32
