@@ -49,7 +49,9 @@ typedef struct {
 /* RMSNorm with the residual's addition and an 8-bit output: per row
  *     x'    = round(x + delta)     to dtype (x' = x when delta is NULL),
  *     n     = x' * gamma / sqrt(mean(x'^2) + eps)      in fp32,
- *     scale = max |n| / 127,   q = n / scale rounded to nearest even.
+ *     scale = max |n| / 127,   q = n / scale rounded to nearest even
+ * (q is formed from x' * gamma, the root cancelling: of bf16 and fp16 rows it is
+ * the exact quotient's integer).
  *   x, delta: dtype [T][H] (delta may be NULL);  gamma: dtype [H]
  *   x_sum: dtype [T][H] or NULL; out: x' (the residual stream).  May be x or
  *          delta itself (same pointer and stride).

@@ -238,17 +238,6 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// (a, b) * (c, d) in one operation
-__device__ __forceinline__ void mul2(float &a, float &b, float c, float d) {
-  asm("{\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%0, %1};\n\t"
-      "mov.b64 y, {%2, %3};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\t"
-      "mov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "f"(c), "f"(d));
-}
-
 // silu for results of 16 bits from the hardware approximations (relative error
 // near 2^-21); with the exact exponential and division for fp32 results.
 template <typename T>

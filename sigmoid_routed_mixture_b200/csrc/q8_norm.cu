@@ -5,6 +5,12 @@
 // Sums and statistics are fp32; x' is rounded to the stream's type because
 // that is the value the stream stores, and the norm reads the stored value.
 //
+// The root cancels in n / scale.  It is split into a power of two p and a
+// factor r, 1 <= r < 2; u = x' p gamma is exact in fp32 for 16-bit types (8 + 8
+// and 11 + 11 bits), n = u r, and q = rne(127 u / max |u|) is the definition's
+// integer, ties included.  (From n rounded to fp32, one q in 10^5 went to the
+// neighbour.)
+//
 // One read of the row: a group of TPR threads holds a whole row in registers
 // (U loads of E elements a thread) through its two reductions, the sum of
 // squares and the maximum, so the bytes are the floor's.  Rows that do not fit
@@ -48,46 +54,73 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *buf) {
   return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < n ? buf[threadIdx.x & 31] : 0u);
 }
 
-// scale and the factor 127 / max that takes n to q, as the sum of two fp32
+// 1 / sqrt(mean square + eps) of a row as p * r, p a power of two, 1 <= r < 2.
+// sum(f): this thread's part of the sum of squares of the row times f.  `up`: 1,
+// or the power of two that the row has to be multiplied by first (exactly: only
+// rows below 2^-40 have one).
+struct Root {
+  float p, r, up;
+};
+template <int kWarps, typename Sum>
+__device__ __forceinline__ Root inv_root(Sum sum, float H, float eps, float (*buf)[32]) {
+  float f = 1.f;
+  float ms = row_sum<kWarps>(sum(1.f), buf[0]) / H + eps;
+  if (!(ms >= 0x1p-100f && ms <= 0x1p120f)) {
+    // the squares left fp32's range (the same decision in the whole row): once
+    // more with the row under a power of two
+    f = ms < 0x1p-100f ? 0x1p96f : 0x1p-96f;
+    ms = row_sum<kWarps>(sum(f), buf[1]) / H + (eps * f) * f;
+  }
+  const float inv = 1.0f / sqrtf(ms);
+  Root o;
+  // (0 gives p = 0, r = 1; an infinity or NaN keeps itself as p)
+  o.p = inv <= 0x1p126f ? __uint_as_float(__float_as_uint(inv) & 0x7f800000u) : inv;
+  o.r = __uint_as_float((__float_as_uint(inv) & 0x007fffffu) | 0x3f800000u);
+  o.up = f > 1.f ? f : 1.f;
+  if (f < 1.f) o.p *= f;
+  return o;
+}
+
+// scale and the factor 127 / max that takes u to q, as the sum of two fp32
 // numbers, for rows multiplied by `up`: 1, or the power of two that brings rows
-// below 2^-100 or above 2^100 away from the ends of fp32's range.  Both are 0
-// for a zero row; a row with an infinity or NaN gets scale NaN and zeros.
+// below 2^-100 or above 2^100 away from the ends of fp32's range.  max_bits: max
+// |u|, n = u * r.  Both are 0 for a zero row; a row whose n holds an infinity or
+// NaN gets scale NaN and zeros.
 struct QFactor {
-  float hi, lo;
+  float hi, lo, max;
 };
 struct QScale {
   float scale, up;
   QFactor r;
   bool finite;
 };
-__device__ __forceinline__ QScale q_scale(uint32_t max_bits) {
+__device__ __forceinline__ QScale q_scale(uint32_t max_bits, float r = 1.f) {
   QScale s;
-  s.finite = max_bits < 0x7f800000u;
-  const float m = __uint_as_float(max_bits);
-  s.scale = s.finite ? m / 127.f : __uint_as_float(0x7fc00000u);
+  const float m = __uint_as_float(max_bits), n = m * r;
+  s.finite = abs_bits(n) < 0x7f800000u;
+  s.scale = s.finite ? n / 127.f : __uint_as_float(0x7fc00000u);
   s.up = m < 0x1p-100f ? 0x1p100f : m > 0x1p100f ? 0x1p-100f : 1.f;
-  s.r = {0.f, 0.f};
+  s.r = {0.f, 0.f, 0.f};
   if (s.finite && m > 0.f) {
     const float mu = m * s.up;
+    s.r.max = mu;
     s.r.hi = 127.f / mu;
     s.r.lo = fmaf(-s.r.hi, mu, 127.f) * (s.r.hi * (1.f / 127.f));  // a few bits of it count
   }
   return s;
 }
 
-// q = rne(n * 127 / max) in the low byte: n * hi + (n * lo) is within one
-// rounding of the quotient, and adding 1.5 * 2^23 rounds that to the nearest
-// integer, ties to even, in two's complement; the quotient is at most 127, so
-// nothing has to be clamped.  Without `lo` a quotient of exactly k + 1/2 went
-// to the wrong side when hi was rounded that way, one element in 70000 of fp16
-// rows.  With it such an n gives exactly k + 1/2: say hi is 127 / max (1 + d),
-// |d| <= 2^-24.  The product n * hi is then either k + 1/2, with |(k + 1/2) d|
-// at most half a unit of its last place, or the neighbour, with at least half
-// a unit; adding n * lo = -(k + 1/2) d leaves less than half a unit to
-// k + 1/2 each time.  (The last places below 1/2 are half as wide, but there
-// 1/2 and its lower neighbour both round to 0.)
+// q = rne(n * 127 / max) in the low byte: n * hi + (n * lo) is the quotient
+// rounded once to fp32 (what is lost before is 2^-46 of it), and adding
+// 1.5 * 2^23 rounds that to the nearest integer, ties to even, in two's
+// complement; the quotient is at most 127, so nothing has to be clamped.  A
+// quotient of exactly k + 1/2 comes out as that, and one that is not is at least
+// 1 / (254 m) of itself away from it, where n is m < 2^a units of its last bit:
+// for a <= 16 (bf16 products) more than half a unit of fp32's last place, so it
+// does not.  (By hi alone one element in 70000 of fp16 rows went astray.)
+__device__ __forceinline__ float quotient(float n, QFactor r) { return fmaf(n, r.hi, n * r.lo); }
 __device__ __forceinline__ uint32_t q_bits(float n, QFactor r) {
-  return __float_as_uint(fmaf(n, r.lo, n * r.hi) + 12582912.f);
+  return __float_as_uint(quotient(n, r) + 12582912.f);
 }
 __device__ __forceinline__ void q_bits2(float n0, float n1, QFactor r, uint32_t &q0, uint32_t &q1) {
   asm("{\n\t.reg .b64 n, h, l, c;\n\t"
@@ -95,8 +128,8 @@ __device__ __forceinline__ void q_bits2(float n0, float n1, QFactor r, uint32_t 
       "mov.b64 h, {%4, %4};\n\t"
       "mov.b64 l, {%5, %5};\n\t"
       "mov.b64 c, {%6, %6};\n\t"
-      "mul.rn.f32x2 h, n, h;\n\t"
-      "fma.rn.f32x2 h, n, l, h;\n\t"
+      "mul.rn.f32x2 l, n, l;\n\t"
+      "fma.rn.f32x2 h, n, h, l;\n\t"
       "add.rn.f32x2 h, h, c;\n\t"
       "mov.b64 {%0, %1}, h;\n\t}"
       : "=r"(q0), "=r"(q1)
@@ -107,24 +140,93 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// E consecutive q of a row that is finite (n multiplied by up).
-template <int E>
-__device__ __forceinline__ void store_q(int8_t *p, const float (&n)[E], QFactor r) {
+// fp16 products have 22 bits: a quotient beside k + 1/2 may come out as k + 1/2,
+// though never on its other side.  `most` collects the distance of the quotients
+// from their integers, and if one is 1/2 the thread goes through its elements
+// once more with settle() (one element in 400,000, ties included).
+__device__ __forceinline__ void q_near2(float n0, float n1, QFactor r, uint32_t &q0, uint32_t &q1, float &most) {
+  float d0, d1;
+  asm("{\n\t.reg .b64 n, h, l, c, s;\n\t"
+      "mov.b64 n, {%4, %5};\n\t"
+      "mov.b64 h, {%6, %6};\n\t"
+      "mov.b64 l, {%7, %7};\n\t"
+      "mov.b64 c, {%8, %8};\n\t"
+      "mul.rn.f32x2 l, n, l;\n\t"
+      "fma.rn.f32x2 h, n, h, l;\n\t"
+      "add.rn.f32x2 s, h, c;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t"
+      "sub.rn.f32x2 s, s, c;\n\t"
+      "sub.rn.f32x2 h, h, s;\n\t"
+      "mov.b64 {%2, %3}, h;\n\t}"
+      : "=r"(q0), "=r"(q1), "=f"(d0), "=f"(d1)
+      : "f"(n0), "f"(n1), "f"(r.hi), "f"(r.lo), "f"(12582912.f));
+  most = fmaxf(most, fmaxf(fabsf(d0), fabsf(d1)));
+}
+__device__ __forceinline__ uint32_t q_near(float n, QFactor r, float &d) {
+  const float x = quotient(n, r), s = x + 12582912.f;
+  d = x - (s - 12582912.f);
+  return __float_as_uint(s);
+}
+// q of a quotient near c = k + 1/2: whether 254 |n| is more than, equal to (to
+// even) or less than 2 c max.  Both products are exact as two fp32 numbers, and
+// so is their difference, the leading parts being within a factor of two.
+__device__ __forceinline__ uint32_t settle(float n, QFactor r, uint32_t q, float d) {
+  const float c2 = fabsf(2.f * (__uint_as_float(q) - 12582912.f) + copysignf(1.f, d));
+  const float a = __fmul_rn(254.f, fabsf(n)), b = __fmul_rn(c2, r.max);
+  const float more = __fsub_rn(a, b) + (fmaf(254.f, fabsf(n), -a) - fmaf(c2, r.max, -b));
+  int k = static_cast<int>(c2) >> 1;
+  if (more > 0.f || (more == 0.f && (k & 1))) ++k;
+  return static_cast<uint32_t>(n < 0.f ? -k : k);
+}
+// An element's q again, where it may have gone to the wrong side.
+__device__ __forceinline__ void settle_q(int8_t *p, float n, QFactor r) {
+  float d;
+  const uint32_t q = q_near(n, r, d);
+  if (fabsf(d) == 0.5f) *p = static_cast<int8_t>(settle(n, r, q, d));
+}
+
+// E consecutive q of a row that is finite (n multiplied by up).  kNear: with `most`.
+template <int E, bool kNear>
+__device__ __forceinline__ void store_q(int8_t *p, const float (&n)[E], QFactor r, float &most) {
   if constexpr (E == 1) {
-    *p = static_cast<int8_t>(q_bits(n[0], r));
+    float d = 0.f;
+    *p = static_cast<int8_t>(kNear ? q_near(n[0], r, d) : q_bits(n[0], r));
+    most = fmaxf(most, fabsf(d));
   } else {
-    uint32_t w[E / 4];
+    uint32_t q[E], w[E / 4];
 #pragma unroll
-    for (int k = 0; k < E / 4; ++k) {
-      uint32_t q[4];
-      q_bits2(n[4 * k], n[4 * k + 1], r, q[0], q[1]);
-      q_bits2(n[4 * k + 2], n[4 * k + 3], r, q[2], q[3]);
-      w[k] = low_bytes(q[0], q[1], q[2], q[3]);
+    for (int k = 0; k < E; k += 2) {
+      if constexpr (kNear)
+        q_near2(n[k], n[k + 1], r, q[k], q[k + 1], most);
+      else
+        q_bits2(n[k], n[k + 1], r, q[k], q[k + 1]);
     }
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) w[k] = low_bytes(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
     if constexpr (E == 8)
       *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     else
       *reinterpret_cast<uint32_t *>(p) = w[0];
+  }
+}
+
+// E products, two in one operation
+template <int E>
+__device__ __forceinline__ void mul_by(float (&v)[E], float f) {
+  if constexpr (E == 1) {
+    v[0] *= f;
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; k += 2) mul2(v[k], v[k + 1], f, f);
+  }
+}
+template <int E>
+__device__ __forceinline__ void mul_by(float (&v)[E], const float (&f)[E]) {
+  if constexpr (E == 1) {
+    v[0] *= f[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; k += 2) mul2(v[k], v[k + 1], f[k], f[k + 1]);
   }
 }
 
@@ -174,6 +276,7 @@ template <typename T, int E, int U, int kWarps>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     q8_rows_kernel(const Q8RowArgs p) {
   using Io = RowIo<T, E>;
+  constexpr bool kNear = std::is_same<T, Fp16>::value;
   __shared__ float sum_buf[2][32];
   __shared__ uint32_t max_buf[32];
   const int tid = kWarps == 1 ? (threadIdx.x & 31) : threadIdx.x;
@@ -242,35 +345,29 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     for (int j = 0; j < U; ++j)
       if (there(j)) Io::store(x_sum + at(j), v[j]);
   }
+  float r = 1.f;  // n = v * r
   if (gamma) {
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-#pragma unroll
-      for (int k = 0; k < E; ++k) ss = fmaf(v[j][k], kAgain && !own(j) ? 0.f : v[j][k], ss);
-    float ms = row_sum<kWarps>(ss, sum_buf[0]) / static_cast<float>(p.H) + p.eps;
-    if (!(ms >= 0x1p-100f && ms <= 0x1p120f)) {
-      // the squares left fp32's range (the same decision in the whole row):
-      // once more with the row under a power of two
-      const float f = ms < 0x1p-100f ? 0x1p96f : 0x1p-96f;
-      ss = 0.f;
+    auto sum = [&](float f) {
+      float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < U; ++j)
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          v[j][k] *= f;
-          if (own(j)) ss = fmaf(v[j][k], v[j][k], ss);
-        }
-      ms = row_sum<kWarps>(ss, sum_buf[1]) / static_cast<float>(p.H) + (p.eps * f) * f;
+        for (int k = 0; k < E; ++k) ss = fmaf(v[j][k] * f, kAgain && !own(j) ? 0.f : v[j][k] * f, ss);
+      return ss;
+    };
+    const Root root = inv_root<kWarps>(sum, static_cast<float>(p.H), p.eps, sum_buf);
+    r = root.r;
+    if (root.up != 1.f) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) mul_by(v[j], root.up);
     }
-    const float inv = 1.0f / sqrtf(ms);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (there(j)) {
         float g[E];
         Io::unpack(rg[j], g);
-#pragma unroll
-        for (int k = 0; k < E; ++k) v[j][k] = v[j][k] * inv * g[k];
+        mul_by(v[j], root.p);
+        mul_by(v[j], g);
       }
     }
   }
@@ -283,10 +380,17 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
   if (p.y) {
     T *y = static_cast<T *>(p.y) + t * p.ld_y;
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (there(j)) Io::store(y + at(j), v[j]);
+    for (int j = 0; j < U; ++j) {
+      if (there(j)) {
+        float n[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) n[k] = v[j][k];
+        mul_by(n, r);
+        Io::store(y + at(j), n);
+      }
+    }
   }
-  const QScale s = q_scale(row_max<kWarps>(m, max_buf));
+  const QScale s = q_scale(row_max<kWarps>(m, max_buf), r);
   const int64_t to = dst_row(t, p.unit_offset);
   if (tid == 0) p.scale[to] = s.scale;
   int8_t *q = p.q + to * p.ld_q;
@@ -296,9 +400,17 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
 #pragma unroll
       for (int k = 0; k < E; ++k) v[j][k] = s.finite ? v[j][k] * s.up : 0.f;
   }
+  float most = 0.f;
 #pragma unroll
   for (int j = 0; j < U; ++j)
-    if (there(j)) store_q<E>(q + at(j), v[j], s.r);
+    if (there(j)) store_q<E, kNear>(q + at(j), v[j], s.r, most);
+  if (kNear && most == 0.5f) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int k = 0; k < E; ++k)
+        if (there(j)) settle_q(q + at(j) + k, v[j][k], s.r);
+  }
 }
 
 // Quantisation alone.  Threads past the row's end take its last E elements once
@@ -338,6 +450,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
       for (int k = 0; k < E; ++k) v[j][k] = s.finite ? v[j][k] * s.up : 0.f;
   }
   int8_t *q = p.q + to * p.ld_q;
+  float most = 0.f;  // (not used)
   if constexpr (E == 1 && U % 2 == 0) {  // single elements: two of the row's at once
 #pragma unroll
     for (int j = 0; j < U; j += 2) {
@@ -348,7 +461,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < U; ++j) store_q<E>(q + min((j * tpr + tid) * E, last), v[j], s.r);
+    for (int j = 0; j < U; ++j) store_q<E, false>(q + min((j * tpr + tid) * E, last), v[j], s.r, most);
   }
 }
 
@@ -364,6 +477,7 @@ template <typename T, int U, int kWarps, bool kPlain>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     q8_offset_rows_kernel(const Q8RowArgs p) {
   constexpr int E = kVec<T>;
+  constexpr bool kNear = !kPlain && std::is_same<T, Fp16>::value;
   using Io = RowIo<T, E>;
   using Raw = typename Io::Raw;
   __shared__ float sum_buf[2][32];
@@ -417,32 +531,28 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     for (int j = 0; j < U; ++j)
       if (at(j) < hi) store_part<T, E>(x_sum + at(j), v[j], lo - at(j), hi - at(j));
   }
+  float r = 1.f;  // n = v * r
   if (!kPlain && p.gamma) {
-    float ss = 0.f;  // the elements outside the row are zeros
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-#pragma unroll
-      for (int k = 0; k < E; ++k) ss = fmaf(v[j][k], v[j][k], ss);
-    float ms = row_sum<kWarps>(ss, sum_buf[0]) / static_cast<float>(p.H) + p.eps;
-    if (!(ms >= 0x1p-100f && ms <= 0x1p120f)) {  // as in q8_rows_kernel
-      const float f = ms < 0x1p-100f ? 0x1p96f : 0x1p-96f;
-      ss = 0.f;
+    auto sum = [&](float f) {
+      float ss = 0.f;  // the elements outside the row are zeros
 #pragma unroll
       for (int j = 0; j < U; ++j)
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          v[j][k] *= f;
-          ss = fmaf(v[j][k], v[j][k], ss);
-        }
-      ms = row_sum<kWarps>(ss, sum_buf[1]) / static_cast<float>(p.H) + (p.eps * f) * f;
+        for (int k = 0; k < E; ++k) ss = fmaf(v[j][k] * f, v[j][k] * f, ss);
+      return ss;
+    };
+    const Root root = inv_root<kWarps>(sum, static_cast<float>(p.H), p.eps, sum_buf);
+    r = root.r;
+    if (root.up != 1.f) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) mul_by(v[j], root.up);
     }
-    const float inv = 1.0f / sqrtf(ms);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       float g[E];
       Io::unpack(rg[kPlain ? 0 : j], g);
-#pragma unroll
-      for (int k = 0; k < E; ++k) v[j][k] = v[j][k] * inv * g[k];
+      mul_by(v[j], root.p);
+      mul_by(v[j], g);
     }
   }
   uint32_t m = 0;
@@ -453,10 +563,17 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
   if (!kPlain && p.y) {
     T *y = static_cast<T *>(p.y) + (t * p.ld_y - lo);
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (at(j) < hi) store_part<T, E>(y + at(j), v[j], lo - at(j), hi - at(j));
+    for (int j = 0; j < U; ++j) {
+      if (at(j) < hi) {
+        float n[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) n[k] = v[j][k];
+        mul_by(n, r);
+        store_part<T, E>(y + at(j), n, lo - at(j), hi - at(j));
+      }
+    }
   }
-  const QScale s = q_scale(row_max<kWarps>(m, max_buf));
+  const QScale s = q_scale(row_max<kWarps>(m, max_buf), r);
   if (tid == 0) p.scale[t] = s.scale;
   if (!s.finite || s.up != 1.f) {
 #pragma unroll
@@ -465,16 +582,24 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
       for (int k = 0; k < E; ++k) v[j][k] = s.finite ? v[j][k] * s.up : 0.f;
   }
   int8_t *q = p.q + (t * p.ld_q - lo);
+  float most = 0.f;
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int from = lo - at(j), to = hi - at(j);
     if (from <= 0 && to >= E) {
-      store_q<E>(q + at(j), v[j], s.r);
+      store_q<E, kNear>(q + at(j), v[j], s.r, most);
     } else {
 #pragma unroll
       for (int k = 0; k < E; ++k)
-        if (k >= from && k < to) q[at(j) + k] = static_cast<int8_t>(q_bits(v[j][k], s.r));
+        if (k >= from && k < to) store_q<1, kNear>(q + at(j) + k, {v[j][k]}, s.r, most);
     }
+  }
+  if (kNear && most == 0.5f) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int k = 0; k < E; ++k)
+        if (k >= lo - at(j) && k < hi - at(j)) settle_q(q + at(j) + k, v[j][k], s.r);
   }
 }
 
@@ -483,6 +608,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
 // thread that has just read it, so that they may be x or delta themselves.
 template <typename T>
 __global__ void __launch_bounds__(1024) q8_long_rows_kernel(const Q8RowArgs p) {
+  constexpr bool kNear = std::is_same<T, Fp16>::value;
   __shared__ float sum_buf[2][32];
   __shared__ uint32_t max_buf[32];
   previous_done();
@@ -494,30 +620,33 @@ __global__ void __launch_bounds__(1024) q8_long_rows_kernel(const Q8RowArgs p) {
     const float v = to_float(x[i]);
     return delta ? to_float(from_float<T>(v + to_float(delta[i]))) : v;
   };
-  float f = 1.f, inv = 1.f;
+  Root root = {1.f, 1.f, 1.f};
   if (gamma) {
-    float ss = 0.f;
-    for (int i = threadIdx.x; i < p.H; i += blockDim.x) ss = fmaf(at(i), at(i), ss);
-    float ms = row_sum<32>(ss, sum_buf[0]) / static_cast<float>(p.H) + p.eps;
-    if (!(ms >= 0x1p-100f && ms <= 0x1p120f)) {
-      f = ms < 0x1p-100f ? 0x1p96f : 0x1p-96f;
-      ss = 0.f;
-    for (int i = threadIdx.x; i < p.H; i += blockDim.x) ss = fmaf(at(i) * f, at(i) * f, ss);
-      ms = row_sum<32>(ss, sum_buf[1]) / static_cast<float>(p.H) + (p.eps * f) * f;
-    }
-    inv = 1.0f / sqrtf(ms);
+    auto sum = [&](float f) {
+      float ss = 0.f;
+      for (int i = threadIdx.x; i < p.H; i += blockDim.x) {
+        const float v = at(i) * f;
+        ss = fmaf(v, v, ss);
+      }
+      return ss;
+    };
+    root = inv_root<32>(sum, static_cast<float>(p.H), p.eps, sum_buf);
   }
-  auto normed = [&](int i, float v) { return gamma ? v * f * inv * to_float(gamma[i]) : v; };
+  auto before_r = [&](int i, float v) { return gamma ? v * root.up * root.p * to_float(gamma[i]) : v; };  // u = n / r
   uint32_t m = 0;
-  for (int i = threadIdx.x; i < p.H; i += blockDim.x) m = max(m, abs_bits(normed(i, at(i))));
-  const QScale s = q_scale(row_max<32>(m, max_buf));
+  for (int i = threadIdx.x; i < p.H; i += blockDim.x) m = max(m, abs_bits(before_r(i, at(i))));
+  const QScale s = q_scale(row_max<32>(m, max_buf), root.r);
   const int64_t to = dst_row(t, p.unit_offset);
   if (threadIdx.x == 0) p.scale[to] = s.scale;
   for (int i = threadIdx.x; i < p.H; i += blockDim.x) {
-    const float v = at(i), n = normed(i, v);
+    const float v = at(i), u = before_r(i, v);
     if (p.x_sum) static_cast<T *>(p.x_sum)[t * p.ld_sum + i] = from_float<T>(v);
-    if (p.y) static_cast<T *>(p.y)[t * p.ld_y + i] = from_float<T>(n);
-    p.q[to * p.ld_q + i] = s.finite ? static_cast<int8_t>(q_bits(n * s.up, s.r)) : int8_t(0);
+    if (p.y) static_cast<T *>(p.y)[t * p.ld_y + i] = from_float<T>(u * root.r);
+    const float n[1] = {s.finite ? u * s.up : 0.f};
+    float most = 0.f;
+    int8_t *q = p.q + to * p.ld_q + i;
+    store_q<1, kNear>(q, n, s.r, most);
+    if (kNear && most == 0.5f) settle_q(q, n[0], s.r);
   }
 }
 

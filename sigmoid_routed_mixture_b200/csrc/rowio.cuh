@@ -57,6 +57,17 @@ __device__ __forceinline__ void unpack2(Fp16, uint32_t w, float &lo, float &hi) 
   hi = f.y;
 }
 
+// (a, b) * (c, d) in one operation
+__device__ __forceinline__ void mul2(float &a, float &b, float c, float d) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
 // One 16-byte vector of T and its element count; E = 1 is the form for rows
 // that are not 16-byte aligned.
 template <typename T>

@@ -334,3 +334,28 @@ def test_pack_weights(E, shared):
     for got, scale, w in ((w13, s13, units), (w2q, s2, downs.reshape(G * H, I))):
         q, s = q8.quantize(w)
         assert torch.equal(got, q) and torch.equal(scale, s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,top,power", [(torch.bfloat16, 255, 0), (torch.float16, 2047, -12), (torch.bfloat16, 255, 90),
+                                             (torch.bfloat16, 255, -100)])
+@pytest.mark.parametrize("T,H", [(20000, 256), (3000, 2048), (200, 6144), (2500, 2047), (2500, 385), (150, 16391), (60, 40001)])
+def test_norm_rounds_every_quotient(T, H, dtype, top, power):
+    """n / scale does not depend on the root that n is divided by: of 16-bit rows it is 127 u / max |u| with u the exact
+    product of x and gamma.  Whole x and gamma times powers of two, equality against integer arithmetic; ties to even."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(30)
+    a = (torch.randn(T, H, generator=g, device="cuda") * top / 4).round().clamp(-top, top)
+    b = torch.randint(top // 2, top + 1, (H,), generator=g, device="cuda")
+    less = torch.arange(H, device="cuda") % 5
+    exact = a.double() * torch.tensor([2.0 ** (power - k) for k in range(5)], dtype=torch.float64, device="cuda")[less]
+    x, gamma = exact.to(dtype), (b.double() / (top + 1)).to(dtype)
+    assert torch.equal(x.double(), exact) and torch.equal(gamma.double() * (top + 1), b.double())
+    q, scale = q8.add_rmsnorm(x, gamma, 0.0)
+    u = a.long() * b * 2 ** (4 - less)
+    M = u.abs().amax(1, keepdim=True)
+    twice = 254 * u.abs() + M  # twice M times (the quotient + 1/2)
+    want = twice // (2 * M)
+    want -= ((twice % (2 * M) == 0) & (want % 2 == 1)).long()
+    assert torch.equal(q.long(), want * u.sign())
+    check(x, reference(x, gamma, 0.0)[1], q, scale)
