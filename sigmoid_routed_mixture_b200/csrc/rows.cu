@@ -8,6 +8,7 @@
 // order.  (The inverse is a maximum of positions, whose order does not matter.)
 #include <type_traits>
 
+#include "grid_walk.h"
 #include "kernels.h"
 #include "launch.cuh"
 #include "rowio.cuh"
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(256)
                        const int32_t *__restrict__ sorted, int32_t *__restrict__ pos) {
   previous_done();
   const int n = row_total(offsets, p.E + 1, p.P, p.err);
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) invert(pos, sorted[i], i, p.P, p.err);
+  grid_walk(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, n, [&](int i) { invert(pos, sorted[i], i, p.P, p.err); });
 }
 
 // The rows by token: each token row is read once and written to its positions

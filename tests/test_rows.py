@@ -6,6 +6,8 @@ fused with its addition, is off by at most n u sum |terms|; one more for the res
 A gradient of a weight is a dot product over H: a lane's chain of fused products, five shuffles and at most eight
 partial sums, H / 32 + 13 at most: (H / 32 + 13) u sum |terms|."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -73,6 +75,36 @@ def test_binding_refuses_host_tensors():
     cfg = rows.Config(4, 8, 4, 2)
     with pytest.raises(ValueError, match="CUDA"):
         rows.sort(cfg, torch.zeros(4, 8, dtype=torch.bfloat16), None, None, None)
+
+
+def test_walk_of_the_inverse_stays_in_range(tmp_path):
+    """rows_invert_kernel's indices over the last two steps of the grid, up to as many positions as are accepted
+    (2^31 - 1): each once and none outside."""
+    src, exe = tmp_path / "walk.cpp", tmp_path / "walk"
+    src.write_text("""#include <cstdlib>
+#include <initializer_list>
+#include "grid_walk.h"
+int main() {
+  const int64_t step = 8 * 148 * 256;
+  for (int64_t n : {(int64_t(1) << 31) - 1, (int64_t(1) << 31) - step, int64_t(2147400000), int64_t(1000003)}) {
+    const int64_t start = (n / step > 1 ? n / step - 1 : 0) * step;
+    int64_t seen = 0, sum = 0;
+    for (int64_t first = 0; first < step; ++first) {
+      srm::grid_walk(start + first, step, n, [&](int i) {
+        if (i < start || i >= n) std::exit(2);
+        ++seen;
+        sum += i - start;
+      });
+    }
+    const int64_t m = n - start;
+    if (seen != m || sum != m * (m - 1) / 2) return 1;
+  }
+  return 0;
+}
+""")
+    csrc = os.path.join(os.path.dirname(moe.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)], timeout=60).returncode == 0
 
 
 # ------------------------------------------------------------------ on the GPU
