@@ -67,9 +67,8 @@ __device__ __forceinline__ int row_total(const int32_t *offsets, int groups_end,
   return 0;
 }
 
-// pos[a] as a position in [0, P), or -1.
-__device__ __forceinline__ int row_pos(const int32_t *pos, int a, int P, int *err) {
-  const int p = pos[a];
+// p as a position in [0, P), or -1.
+__device__ __forceinline__ int row_pos(int p, int P, int *err) {
   if (p >= -1 && p < P) return p;
   record_error(err, MOE_ERR_BAD_INDEX);
   return -1;
@@ -89,8 +88,8 @@ constexpr int kSmallPositions = 4096;  // the inverse in every CTA's shared memo
 
 // pos[sorted[p]] = p over the positions that hold a row (pos is -1 before).
 __global__ void __launch_bounds__(256)
-    rows_invert_kernel(const RowsArgs p, const int32_t *__restrict__ offsets,
-                       const int32_t *__restrict__ sorted, int32_t *__restrict__ pos) {
+    rows_invert_kernel(const RowsArgs p, const int32_t *offsets,
+                       const int32_t *sorted, int32_t *pos) {
   previous_done();
   const int n = row_total(offsets, p.E + 1, p.P, p.err);
   grid_walk(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, n, [&](int i) { invert(pos, sorted[i], i, p.P, p.err); });
@@ -114,9 +113,9 @@ __device__ __forceinline__ void scatter_tokens(const RowsArgs &p, const int32_t 
     // lane k holds the token's k-th position, the shared row's behind the slots
     int mine = -1;
     if (lane < p.K)
-      mine = row_pos(pos, t * p.K + lane, p.P, p.err);
+      mine = row_pos(pos[t * p.K + lane], p.P, p.err);
     else if (lane == p.K && p.has_shared)
-      mine = row_pos(pos, p.T * p.K + t, p.P, p.err);
+      mine = row_pos(pos[p.T * p.K + t], p.P, p.err);
     if (xs_scale && begin == 0 && mine >= 0) xs_scale[mine] = x_scale[t];
     const int n_dst = p.K + p.has_shared;
     const W *src = reinterpret_cast<const W *>(x + t * x_pitch);
@@ -151,9 +150,9 @@ __device__ __forceinline__ void scatter_tokens(const RowsArgs &p, const int32_t 
 
 template <typename W>
 __global__ void __launch_bounds__(256)
-    rows_scatter_kernel(const RowsArgs p, const int32_t *__restrict__ pos, const uint8_t *__restrict__ x,
-                        uint8_t *__restrict__ xs, const float *__restrict__ x_scale,
-                        float *__restrict__ xs_scale, int64_t row_bytes, int64_t x_pitch, int64_t xs_pitch,
+    rows_scatter_kernel(const RowsArgs p, const int32_t *pos, const uint8_t *x,
+                        uint8_t *xs, const float *x_scale,
+                        float *xs_scale, int64_t row_bytes, int64_t x_pitch, int64_t xs_pitch,
                         int wpt) {
   previous_done();
   scatter_tokens<W>(p, pos, x, xs, x_scale, xs_scale, row_bytes, x_pitch, xs_pitch, wpt);
@@ -164,10 +163,10 @@ __global__ void __launch_bounds__(256)
 // (64 tokens x 9 rows of 12 KB: 8.4 us as clear, invert and scatter.)
 template <typename W>
 __global__ void __launch_bounds__(256)
-    rows_sort_small_kernel(const RowsArgs p, const int32_t *__restrict__ offsets,
-                           const int32_t *__restrict__ sorted, int32_t *__restrict__ pos,
-                           const uint8_t *__restrict__ x, uint8_t *__restrict__ xs,
-                           const float *__restrict__ x_scale, float *__restrict__ xs_scale, int64_t row_bytes,
+    rows_sort_small_kernel(const RowsArgs p, const int32_t *offsets,
+                           const int32_t *sorted, int32_t *pos,
+                           const uint8_t *x, uint8_t *xs,
+                           const float *x_scale, float *xs_scale, int64_t row_bytes,
                            int64_t x_pitch, int64_t xs_pitch, int wpt) {
   __shared__ int32_t inverse[kSmallPositions];
   for (int i = threadIdx.x; i < p.P; i += 256) inverse[i] = -1;
@@ -198,24 +197,31 @@ __global__ void __launch_bounds__(256)
 // that has all its rows takes straight-line code.
 template <typename Tt, typename Ts, int E, int NB, bool kExact>
 __global__ void __launch_bounds__(256)
-    rows_unsort_kernel(const RowsArgs p, const Ts *__restrict__ ys, const float *__restrict__ gate,
-                       const int32_t *__restrict__ pos, const Tt *residual, Tt *y, int tpr_log2) {
+    rows_unsort_kernel(const RowsArgs p, const Ts *ys, const float *gate,
+                       const int32_t *pos, const Tt *residual, Tt *y, int tpr_log2) {
   const int tpr = 1 << tpr_log2;
   const int64_t t64 = (static_cast<int64_t>(blockIdx.x) << (8 - tpr_log2)) + (threadIdx.x >> tpr_log2);
   if (t64 >= p.T) return;
   previous_done();
   const int t = static_cast<int>(t64);
   const int n = kExact ? NB : p.K + p.has_shared;
+  // all on their way before the first check
   int at[NB];
   float g[NB];
-  bool all = true;
 #pragma unroll
   for (int k = 0; k < NB; ++k) {
     at[k] = -1;
     g[k] = 1.f;
     if (k < n) {
-      at[k] = row_pos(pos, k < p.K ? t * p.K + k : p.T * p.K + t, p.P, p.err);
+      at[k] = pos[k < p.K ? t * p.K + k : p.T * p.K + t];
       if (gate && k < p.K) g[k] = gate[static_cast<int64_t>(t) * p.K + k];
+    }
+  }
+  bool all = true;
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    if (k < n) {
+      at[k] = row_pos(at[k], p.P, p.err);
       all = all && at[k] >= 0;
     }
   }
@@ -264,8 +270,8 @@ __global__ void __launch_bounds__(256)
 // slot's row already on its way.
 template <typename Tt, typename Ts, int E>
 __global__ void __launch_bounds__(256)
-    rows_unsort_grad_kernel(const RowsArgs p, const Tt *__restrict__ dy, const Ts *ys,
-                            const float *__restrict__ gate, const int32_t *__restrict__ pos, Ts *dys,
+    rows_unsort_grad_kernel(const RowsArgs p, const Tt *dy, const Ts *ys,
+                            const float *gate, const int32_t *pos, Ts *dys,
                             float *dgate, int wpt) {
   constexpr int B = E == 1 ? 16 : 4;
   __shared__ float partial[8][16];
@@ -283,10 +289,10 @@ __global__ void __launch_bounds__(256)
     int mine = -1;  // lane k: the token's k-th position (k <= 16)
     float my_gate = 1.f;
     if (lane < p.K) {
-      mine = row_pos(pos, t * p.K + lane, p.P, p.err);
+      mine = row_pos(pos[t * p.K + lane], p.P, p.err);
       if (gate) my_gate = gate[static_cast<int64_t>(t) * p.K + lane];
     } else if (lane == p.K && p.has_shared) {
-      mine = row_pos(pos, p.T * p.K + t, p.P, p.err);
+      mine = row_pos(pos[p.T * p.K + t], p.P, p.err);
     }
     auto chunk = [&](int u0, auto full) {
       constexpr bool kFull = decltype(full)::value;

@@ -107,6 +107,19 @@ int main() {
     assert subprocess.run([str(exe)], timeout=60).returncode == 0
 
 
+def test_overlapped_kernels_promise_nothing_about_their_inputs():
+    """A kernel that starts before the one ahead of it has ended may not call its inputs constant for its lifetime:
+    files that launch this way have no __restrict__ pointers and no loads by the read-only path."""
+    csrc = os.path.join(os.path.dirname(moe.LIB_PATH), "csrc")
+    texts = {n: open(os.path.join(csrc, n)).read() for n in os.listdir(csrc)}
+    files = [n for n in texts if "previous_done()" in texts[n] and n != "launch.cuh"]
+    assert len(files) >= 3
+    for n in files:
+        code = "\n".join(line.split("//")[0] for line in texts[n].splitlines())
+        for word in ("__restrict__", "__ldg", "global.nc"):
+            assert word not in code, (n, word)
+
+
 # ------------------------------------------------------------------ on the GPU
 
 def gen(seed):
