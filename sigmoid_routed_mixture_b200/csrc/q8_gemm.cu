@@ -228,14 +228,16 @@ __device__ __forceinline__ bool saturated(uint32_t largest) {  // an infinity in
   return (largest & 0x7fffu) == 0x7c00u || (largest >> 16 & 0x7fffu) == 0x7c00u;
 }
 
-// Arrive on the leader's mbarrier when the accumulator has been read.  It
-// orders this warp's tensor-memory loads, which have completed and are fenced,
-// and its reads of the ring slot, whose values are in registers; the results
-// are read by later launches only.  A release at cluster scope would first
-// wait for the warp's stores of the results to reach L2: with it 4096 x 6144 x
-// 1536 takes 85.4k cycles, without 74.1k.
+// Arrive on the leader's mbarrier when the accumulator and the ring slot have
+// been read.  The arrival and the wait for it have cluster scope, but it
+// releases nothing: no memory is handed over (the results are read by later
+// launches only), and what may be overwritten afterwards has been read by then
+// not by the barrier's order but by completion, of the tensor-memory loads by
+// their wait and fence, of the ring slot's by the branch on its values.  A
+// release at cluster scope would first wait for the warp's stores of the results
+// to reach L2: with it 4096 x 6144 x 1536 takes 85.4k cycles, without 74.1k.
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // silu for results of 16 bits from the hardware approximations (relative error
@@ -448,7 +450,7 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
           if (!any_left) break;
         }
         const uint32_t idesc = idesc_i8(C::W_BLOCK, c.n);
-        if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
+        if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag, p.err, kPair)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BT;
         bool ok = true;
@@ -508,7 +510,7 @@ __device__ __forceinline__ void gemm_body(const Q8Maps &tmaps, const Q8GemmArgs 
     if (leader && !cut) {
       uint32_t ps = 0, pph = 0, dph = 0;  // next ring slot and its phase, the producer's signal's
       for (int t = unit;;) {
-        if (!mbar_wait(&s.tile_empty[ps], pph ^ 1u, abort_flag, p.err)) break;
+        if (!mbar_wait(&s.tile_empty[ps], pph ^ 1u, abort_flag, p.err, kPair)) break;
         if (lane == 0) {
           // the other roles (and the peer) get the tile's place worked out
           Tile c;

@@ -7,6 +7,7 @@ exponential is off by its argument's rounding, at most 2 |g| u, and the approxim
 8 u (fp32): (14 + 6 |g|) u + 2^-21 together.  The approximate reciprocal drops sigmoids below 2^-126."""
 import ctypes
 import os
+import re
 import subprocess
 
 import pytest
@@ -75,6 +76,16 @@ def test_headers_are_plain_c(tmp_path):
     subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", inc, str(src), "-L", lib_dir, "-lsrm_moe",
                     "-Wl,-rpath," + lib_dir, "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_arrivals_on_another_cta_have_cluster_scope():
+    """mbarrier.arrive on a shared::cluster address is of CTA scope where it names none, and says nothing to the CTA
+    that it is for."""
+    csrc = os.path.join(os.path.dirname(moe.LIB_PATH), "csrc")
+    found = []
+    for name in os.listdir(csrc):
+        found += re.findall(r'"(mbarrier\.arrive[^ ]*shared::cluster[^ ]*)', open(os.path.join(csrc, name)).read())
+    assert len(found) >= 2 and all(".cluster.shared::cluster" in f for f in found), found
 
 
 # ------------------------------------------------------------------ on the GPU
