@@ -89,7 +89,7 @@ moe_status_t moe_q8_pack_weights(const moe_cfg_t *cfg, const void *w1, const voi
                                  float *w13_scale, int8_t *w2_q, float *w2_scale, void *stream);
 
 /* Shape of a product: R rows of K elements times `groups` weight matrices of N
- * channels.  0 <= R < 2^31 - 1024 (R == 0 is a no-op), 1 <= N, groups * N < 2^31,
+ * channels.  0 <= R < 2^31 - 1024 (R == 0 is a no-op), 1 <= N, groups * N <= 2^31 - 256,
  * 16 <= K <= 65536 and K % 16 == 0, 1 <= groups <= 257.
  *   swiglu: 0, or 1: the channels are units of 16 gate and the 16 matching up
  *           channels (moe_q8_pack_weights' w13; N % 32 == 0) and the result is

@@ -77,8 +77,9 @@ moe_status_t check_matmul(const moe_q8_matmul_t *c) {
   if (c->R < 0 || c->N < 1 || c->K < 1 || c->groups < 1 || !float_dtype(c->dtype)) return MOE_ERR_ARG;
   if (c->swiglu != 0 && c->swiglu != 1) return MOE_ERR_ARG;
   if (c->K % 16 != 0 || c->K > 65536 || (c->swiglu && c->N % 32 != 0)) return MOE_ERR_UNSUPPORTED;
+  // rows and channels are 32-bit numbers, up to a tile's end
   if (c->groups > srm::kQ8MaxGroups || c->R >= (int64_t(1) << 31) - 1024 ||
-      static_cast<int64_t>(c->groups) * c->N >= (int64_t(1) << 31))
+      static_cast<int64_t>(c->groups) * c->N > (int64_t(1) << 31) - 256)
     return MOE_ERR_UNSUPPORTED;
   // tile numbers are 32-bit
   const srm::Q8Plan p = srm::q8_plan(c->R, c->N, c->K, c->groups, num_sms());

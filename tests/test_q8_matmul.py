@@ -64,6 +64,17 @@ def test_pointers_refused():
     assert q8.lib().moe_q8_matmul(None, A, A, A, A, A, None, A, A, 1 << 40, None) == 1
 
 
+@pytest.mark.parametrize("groups,N", [(1, 2 ** 31 - 1), (1, 2 ** 31 - 127), (1, 2 ** 31 - 255), (2, 2 ** 30 - 1),
+                                      (257, (2 ** 31 - 1) // 257)])
+def test_channels_whose_tiles_pass_31_bits_refused(groups, N):
+    """The last tile's end has to be a 32-bit number: N + 127 wrapped, there were no tiles, and y was not written."""
+    c = c_cfg(R=3, N=N, K=16, groups=groups)
+    assert q8.lib().moe_q8_matmul_workspace_size(ctypes.byref(c)) == 0
+    assert call(c) == 2
+    most = (2 ** 31 - 256) // groups
+    assert q8.lib().moe_q8_matmul_workspace_size(ctypes.byref(c_cfg(R=3, N=most, K=16, groups=groups))) > 0
+
+
 def test_headers_are_plain_c(tmp_path):
     src = tmp_path / "client.c"
     src.write_text('#include "srm_rows.h"\n#include "srm_q8.h"\n'
