@@ -171,6 +171,31 @@ def test_dense_swiglu(R, N, K):
         dense(R, N, K, dtype, swiglu=True, seed=i)
 
 
+# 48 MB of token rows are 3 token blocks of a pair, 12 of a single CTA: a whole chunk of them and a part of one
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,N", [(1100, 1100), (1100, 4300), (1100, 300), (1664, 4300)])
+def test_long_rows_in_chunks_of_token_blocks(R, N):
+    dense(R, N, 65536, torch.bfloat16, residual=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,rows", [(40, 1000), (3, 2500)])  # single CTAs, pairs
+def test_one_group_in_chunks(G, rows):
+    K, N = 65536, 300
+    counts = [3] * G
+    counts[G // 2] = rows
+    g, R = gen(12), sum(counts)
+    cfg = q8.MatmulConfig(R, N, K, groups=G, dtype=torch.float32)
+    x, w, xs, ws = ints(g, R, K), ints(g, G * N, K), scales(g, R), scales(g, G * N, 0.1 / K ** 0.5)
+    work, off = q8.workspace(cfg), offsets_of(counts)
+    out = torch.full((R, N), 7.0, device="cuda")
+    q8.matmul(cfg, x, xs, w, ws, work, offsets=off, out=out)
+    edges = off.tolist()
+    for i, (a, b) in enumerate(zip(edges, edges[1:])):
+        check(out[a:b], x[a:b], xs[a:b], w[i * N:(i + 1) * N], ws[i * N:(i + 1) * N])
+    assert moe.device_error(work) == 0
+
+
 def offsets_of(counts):
     off = torch.zeros(len(counts) + 1, dtype=torch.int32, device="cuda")
     off[1:] = torch.tensor(counts, device="cuda").cumsum(0)

@@ -270,6 +270,45 @@ def test_strides(ld, offset):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T,H,ld,offset", [(41, 64, 72, 0), (41, 64, 67, 3), (1200, 37, 40, 1), (5, 4099, 4104, 8)])
+def test_nothing_beside_the_rows_is_written(T, H, ld, offset, dtype):
+    """Strided results inside larger buffers, and positions that no row holds: all else stays as it was."""
+    E, K = 6, 2
+    cfg = rows.Config(T, H, E, K, True, dtype, dtype)
+    gate, offsets, ids, pos = routing(T, E, K, True, 17)
+    offsets, pos = offsets.clone(), pos.clone()
+    offsets[E + 1] -= 2  # the last two positions hold no row
+    pos[ids[-2:].long()] = -1
+    g, ws = gen(18), rows.workspace()
+
+    def buffer(n):
+        flat = torch.randn(n * ld + offset + 5, generator=g, device="cuda").to(dtype)
+        return flat, flat.as_strided((n, H), (ld, 1), offset)
+
+    def others(flat, n):
+        """All of a buffer but the view's first n rows."""
+        keep = torch.ones(flat.numel(), dtype=torch.bool, device="cuda")
+        keep.as_strided((n, H), (ld, 1), offset).fill_(False)
+        return flat[keep]
+
+    x, ys, dy = buffer(T)[1], buffer(cfg.rows)[1], buffer(T)[1]
+    held = cfg.rows - 2
+    for n, call in ((held, lambda out: rows.sort(cfg, x, offsets, ids, ws, out=out)),
+                    (T, lambda out: rows.unsort(cfg, ys, gate, pos, ws, out=out)),
+                    (T, lambda out: rows.sort_grad(cfg, ys, pos, ws, out=out)),
+                    (held, lambda out: rows.unsort_grad(cfg, dy, ys, gate, pos, ws, out=out))):
+        flat, view = buffer(T if n == T else cfg.rows)
+        before = flat.clone()
+        call(view)
+        assert torch.equal(others(flat, n), others(before, n))
+        plain = call(torch.zeros(view.shape, dtype=dtype, device="cuda"))
+        plain = plain[0] if isinstance(plain, tuple) else plain
+        assert torch.equal(view[:n], plain[:n])
+    assert moe.device_error(ws) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [300, 900])  # the inverse in one launch, and in several
 def test_after_permute_with_ids_out_of_range(T):
     """moe_permute skips and flags an id out of range: its assignment has no row, and adds nothing."""
