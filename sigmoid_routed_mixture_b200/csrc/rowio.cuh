@@ -1,5 +1,5 @@
 // rowio.cuh -- element types of the row kernels (q8_norm.cu, rows.cu,
-// q8_gemm.cu): loads and stores of E consecutive elements as fp32 values.
+// q8_gemm.cu): E consecutive elements as loaded and as fp32 values, and stores.
 #pragma once
 
 #include "common.cuh"
@@ -81,9 +81,6 @@ struct RowIo {  // E = kVec<T>, 16-bit types
 #pragma unroll
     for (int k = 0; k < 4; ++k) unpack2(T{}, w[k], f[2 * k], f[2 * k + 1]);
   }
-  static __device__ __forceinline__ void load(const T *p, float (&f)[E]) {
-    unpack(*reinterpret_cast<const uint4 *>(p), f);
-  }
   static __device__ __forceinline__ void store(T *p, const float (&f)[E]) {
     *reinterpret_cast<uint4 *>(p) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
                                                pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
@@ -98,9 +95,6 @@ struct RowIo<float, 4> {
     f[2] = __uint_as_float(r.z);
     f[3] = __uint_as_float(r.w);
   }
-  static __device__ __forceinline__ void load(const float *p, float (&f)[4]) {
-    unpack(*reinterpret_cast<const uint4 *>(p), f);
-  }
   static __device__ __forceinline__ void store(float *p, const float (&f)[4]) {
     *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
   }
@@ -109,7 +103,6 @@ template <typename T>
 struct RowIo<T, 1> {
   using Raw = T;
   static __device__ __forceinline__ void unpack(const T &r, float (&f)[1]) { f[0] = to_float(r); }
-  static __device__ __forceinline__ void load(const T *p, float (&f)[1]) { f[0] = to_float(*p); }
   static __device__ __forceinline__ void store(T *p, const float (&f)[1]) { *p = from_float<T>(f[0]); }
 };
 
