@@ -1,6 +1,7 @@
 // host_util.h -- host-side helpers shared by the C-ABI entry points (api.cu,
-// dsa_api.cu): pointer checks, status mapping, the SM count and tensor-map
-// (TMA descriptor) encoding through the driver entry point.
+// dsa_api.cu, ep_api.cu, q8_api.cu, rows_api.cu): pointer checks, element types,
+// status mapping, the SM count and tensor-map (TMA descriptor) encoding through
+// the driver entry point.
 #pragma once
 
 #include <cuda.h>
@@ -10,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/srm_moe.h"
+#include "../../include/srm_q8.h"
 
 namespace srm {
 namespace host {
@@ -17,6 +19,12 @@ namespace host {
 constexpr int kMaxDevices = 64;
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// of a moe_dtype_t
+inline size_t dtype_size(int32_t d) { return d == MOE_DTYPE_FP32 ? 4 : d == MOE_DTYPE_INT8 ? 1 : 2; }
+inline bool float_dtype(int32_t d) {
+  return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_FP16 || d == MOE_DTYPE_FP32;
+}
 
 inline moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 

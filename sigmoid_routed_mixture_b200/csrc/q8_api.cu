@@ -17,14 +17,6 @@ using namespace srm::host;
 
 constexpr int64_t kMaxLd = int64_t(1) << 40;  // strides x rows stay far inside 64 bits
 
-size_t dtype_size(int32_t d) {
-  return d == MOE_DTYPE_FP32 ? 4 : d == MOE_DTYPE_INT8 ? 1 : 2;
-}
-
-bool float_dtype(int32_t d) {
-  return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_FP16 || d == MOE_DTYPE_FP32;
-}
-
 bool good_ld(int64_t ld, int64_t h) { return ld >= h && ld <= kMaxLd; }
 
 moe_status_t check_rows(const moe_q8_rows_t *c) {

@@ -12,12 +12,6 @@ namespace {
 
 using namespace srm::host;
 
-size_t dtype_size(int32_t d) { return d == MOE_DTYPE_FP32 ? 4 : d == MOE_DTYPE_INT8 ? 1 : 2; }
-
-bool float_dtype(int32_t d) {
-  return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_FP16 || d == MOE_DTYPE_FP32;
-}
-
 moe_status_t check(const moe_rows_cfg_t *c, bool int8_rows, bool slots) {
   if (!c) return MOE_ERR_ARG;
   const bool one_group = c->E == 0 && c->K == 0 && c->has_shared == 1;
