@@ -270,8 +270,8 @@ __device__ __forceinline__ int64_t dst_row(int64_t t, int unit_offset) {
 // Rows whose elements are moved singly (E = 1) take code without a test around
 // every element: threads past the row's end take its last element once more,
 // which only the sum of squares has to leave out; a barrier keeps them from
-// reading it after its owner has stored over it (4096 x 1541 bf16: 40 us with
-// the tests, 25 without).
+// reading it after its owner has stored over it (4096 x 1541 bf16, all elements
+// singly: 40 us with the tests, 25 without when this was taken, 29 now).
 template <typename T, int E, int U, int kWarps>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     q8_rows_kernel(const Q8RowArgs p) {
@@ -471,8 +471,8 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
 // (each row's thread moves its own elements of them singly) and all others are
 // whole vectors.  gamma, which starts anew in each row, is read singly except
 // where it happens to be aligned.  (4096 x 1541 bf16 with sum, norm and 8 bits:
-// 20.4 us, all elements singly 25.7; quantised alone 5003 x 1541 fp16 7.5 against
-// 9.9.)
+// 18.6 us, all elements singly 29; quantised alone 5003 x 1541 fp16 7.3 against
+// 9.5.)
 template <typename T, int U, int kWarps, bool kPlain>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps)
     q8_offset_rows_kernel(const Q8RowArgs p) {
@@ -737,13 +737,18 @@ cudaError_t launch_rows_e(const Q8RowArgs &p, int num_sms, cudaStream_t stream) 
   constexpr int U = E == 1 ? 16 : 4;  // loads a thread: 16 elements at least
   const int loads = (p.H + E - 1) / E;
   if (loads <= 1024 && p.T <= 2 * num_sms) return launch_rows_u<T, E, 1>(p, stream);
-  // (with 1024 threads of 16 single elements the norm spills its registers:
-  // 4096 x 9311 bf16 255 us against 222 in three passes)
+  // (with 1024 threads of 16 single elements the norm keeps much of its row in
+  // local memory: 4096 x 9311 bf16 255 us against 222 in three passes.  With 1024
+  // threads of 4 vectors it keeps 32 to 40 bytes a thread there, in fp32 8, and
+  // 1024 x 24576 bf16 takes 52 us, where three passes over 20001 take 114.)
   if (loads <= U * (E == 1 && !is_plain(p) ? 512 : 1024)) return launch_rows_u<T, E, U>(p, stream);
   return launch_overlapped(q8_long_rows_kernel<T>, static_cast<unsigned>(p.T), 1024, 0, stream, p);
 }
 
-// (512 threads at most: with more the norm spills its registers)
+// (512 threads at most, 16384 elements of 16 bits or 8192 of 32; longer rows are
+// moved singly.  1024 threads of 4 units would keep up to 100 bytes a thread in
+// local memory and still be faster: 1024 x 20001 bf16 51 us against 114, 1024 x
+// 9311 fp32 33 against 60.)
 template <typename T, int U>
 cudaError_t launch_rows_offset(const Q8RowArgs &p, int units, cudaStream_t stream) {
   const int threads = ((units + U - 1) / U + 31) & ~31;
@@ -774,9 +779,17 @@ cudaError_t launch_rows_t(const Q8RowArgs &p, int num_sms, cudaStream_t stream) 
     return !ptr || (reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && (p.T == 1 || ld % E == p.ld_x % E));
   };
   // Short rows, and middling ones that are few, are faster singly: their first
-  // and last units take two steps (bf16 norm, us with / without this: 16384 x
-  // 385 28.8 / 24.5, 16384 x 513 30.2 / 47.4, 1024 x 1001 5.0 / 4.3, 1024 x 1281
-  // 5.4 / 6.3, 4096 x 9311 91 / 224).
+  // and last units take two steps.  One rule for all types and both forms, us by
+  // units / singly (bf16, fp16, fp32):
+  //   norm      16384 x 385    26.3 / 24.7   30.5 / 23.8   19.3 / 23.8
+  //             16384 x 513    27.9 / 52.1   31.9 / 48.5   29.7 / 44.2
+  //             1024 x 1001    5.0 / 4.4     5.9 / 4.6     4.0 / 4.1
+  //             1024 x 1281    5.3 / 6.6     5.4 / 6.4     4.6 / 5.7
+  //   quantise  16384 x 385    11.0 / 7.7    10.6 / 7.5    6.4 / 7.6
+  //             16384 x 513    10.4 / 15.0   9.9 / 14.6    12.0 / 15.4
+  //             1024 x 1001    2.3 / 2.1     2.3 / 2.1     2.1 / 2.2
+  //             16384 x 2047   30.5 / 30.5   30.9 / 31.6   30.4 / 35.9
+  // (fp32 rows would gain from 385 on, 4096 x 9311 bf16 gains most: 90 / 220.)
   const bool gains = p.H > 1024 || (p.H > 512 && p.T > 8 * num_sms);
   const int units = (p.H + 2 * (E - 1)) / E;  // at most, wherever a row starts
   if (gains && p.unit_offset < 0 && whole(p.x, p.ld_x, 16) && whole(p.delta, p.ld_delta, 16) && whole(p.x_sum, p.ld_sum, 16) &&
@@ -793,8 +806,9 @@ cudaError_t launch_dequant_t(const int8_t *q, const float *scale, void *y, int64
   constexpr int E = kVec<T>;
   const bool whole = reinterpret_cast<uintptr_t>(y) % 16 == 0 && reinterpret_cast<uintptr_t>(q) % E == 0;
   const bool vec = whole && H % E == 0 && ld_y % E == 0 && ld_q % E == 0;
-  // (as for the rows to 8 bits: bf16, us with / without: 1024 x 1001 2.2 / 1.9,
-  // 1024 x 1281 2.1 / 2.6, 16384 x 129 3.4 / 4.6, 1 x 6145 1.6 / 2.8)
+  // (as for the rows to 8 bits, us by units / singly, bf16 and fp32: 1024 x 1001
+  // 2.2 / 1.9 and 1.95 / 1.74, 1024 x 1281 2.0 / 2.5 and 2.1 / 2.3, 16384 x 129 3.4 /
+  // 4.4 and 3.3 / 4.2, 1 x 6145 1.7 / 2.8 and 2.1 / 2.8)
   const bool gains = H > 2048 || T_ * H > 5 << 18;
   const bool offset = gains && whole && !vec && (T_ == 1 || ld_y % E == ld_q % E);
   const int loads = vec ? H / E : offset ? (H + 2 * (E - 1)) / E : H;

@@ -410,6 +410,10 @@ cudaError_t launch_unsort_e(const RowsArgs &p, const void *ys, const float *gate
     return launch_overlapped(kern, grid, 256, 0, stream, p, static_cast<const Ts *>(ys), gate, pos,
                              static_cast<const Tt *>(residual), static_cast<Tt *>(y), log2);
   };
+  // Straight-line code for the usual numbers of rows a token, 4 or 8 experts with
+  // and without a shared one; the others test each row.  What the tests cost (us,
+  // straight-line / tested): 16384 tokens x 9 rows of 6144 320 / 642, x 5 178 / 204,
+  // 4096 x 9 of 2048 38.0 / 78.5, x 5 20.3 / 24.9, 64 x 9 of 6144 3.2 / 4.9.
   const int n = p.K + p.has_shared;
   if (n == 4) return go(rows_unsort_kernel<Tt, Ts, E, 4, true>);
   if (n == 5) return go(rows_unsort_kernel<Tt, Ts, E, 5, true>);
