@@ -51,7 +51,7 @@ typedef struct {
  *     n     = x' * gamma / sqrt(mean(x'^2) + eps)      in fp32,
  *     scale = max |n| / 127,   q = n / scale rounded to nearest even
  * (q is formed from x' * gamma, the root cancelling: of bf16 and fp16 rows it is
- * the exact quotient's integer).
+ * the exact quotient's integer, but where products below 2^-126 lose bits).
  *   x, delta: dtype [T][H] (delta may be NULL);  gamma: dtype [H]
  *   x_sum: dtype [T][H] or NULL; out: x' (the residual stream).  May be x or
  *          delta itself (same pointer and stride).
